@@ -1,0 +1,467 @@
+// Matrix product with bias, activation and residual for sm_100a, many rows:
+// tcgen05 on CTA pairs (cta_group::2), bf16 operands (kind::f16) or E4M3 rows
+// with block scales applied by the tensor core (kind::mxf8f6f4.block_scale).
+//
+//   out[m][n] = act(sum_k x[m][k] w[n][k] + bias[n]) + residual[m][n]
+//
+// The tensor cores bound it. Tile: 256 rows x BN features per pair of CTAs, each
+// CTA holding 128 rows of x and BN / 2 features of w per k-block of 128 bytes;
+// the leader issues M = 256, N = BN MMAs, every CTA receives the accumulator of
+// its own 128 rows in its own TMEM, and two accumulators take turns, so that one
+// tile's epilogue runs under the next tile's products.
+//   BN = 256 is for bf16 only (two accumulators fill TMEM); BN = 192 leaves 128
+//   columns, which hold four stages of scales for E4M3. The launch takes
+//   whichever wastes less of the last wave.
+// Tiles are walked in groups of 8 row tiles, feature tiles slowest inside a
+// group, so that the tiles in flight cover a near-square patch of the output and
+// both operands are re-read from L2.
+//   warp 8 (one lane)  TMA producer of its CTA (128-byte swizzled operand boxes,
+//                      for E4M3 also the 512-byte scale tiles: one of x, and two
+//                      that cover the BN features of w in both CTAs); all bytes
+//                      count on the leader's full barrier.
+//   warp 9 (one lane)  leader only: copies the stage's scales into TMEM, then
+//                      issues the MMAs; k-steps past K are not issued, so scale
+//                      bytes past the last block are never used.
+//   warps 0-7          epilogue: warpgroup e takes columns [e BN/2, (e+1) BN/2)
+//                      of the CTA's 128 rows, a thread owns one row and 32
+//                      columns at a time. The residual's 32 x 32 box comes in by
+//                      TMA one step ahead into the staging buffer that the result
+//                      leaves from, so both cross global memory in whole rows; the
+//                      bias goes through 32 floats of shared memory per warp.
+//                      E4M3 output: the 32 columns are one scale block, so a
+//                      thread finds its scale without leaving its registers.
+// Every wait is bounded; a timeout is recorded in the row-operator status word.
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include "pipeline.cuh"
+#include "rows.cuh"
+#include "sm100.cuh"
+
+namespace wf {
+namespace {
+
+using namespace sm100;
+
+constexpr int kThreads = 320;
+constexpr int kEpiWarps = 8;
+constexpr int kProducerWarp = 8;
+constexpr int kMmaWarp = 9;
+constexpr int kBufs = 3;                        // staging buffers per epilogue warp
+constexpr uint32_t kBufBytes = 32 * 64;         // 32 rows x 32 bf16 columns
+constexpr int kGroup = 8;                       // row tiles per raster group
+constexpr int kScaleCols = 384;                 // first TMEM column of the scales
+constexpr uint32_t kABytes = 128 * 128;
+
+template <bool MX, int BN>
+struct Shape {
+  static constexpr uint32_t kBBytes = BN / 2 * 128;
+  static constexpr uint32_t kScaleBytes = MX ? 512 + 1024 : 0;
+  static constexpr uint32_t kStageBytes = kABytes + kBBytes + kScaleBytes;   // per CTA
+  static constexpr int kStages = MX || BN == 256 ? 5 : 6;
+  static constexpr int kKElems = MX ? 128 : 64;        // elements of a k-block
+  static constexpr int kKStep = MX ? 32 : 16;          // elements per MMA
+  // Operands of all stages first (1024-byte aligned for the swizzle), then the
+  // scale tiles, the staging buffers, the bias rows and the barriers.
+  static constexpr uint32_t kOperandBytes = kABytes + kBBytes;
+  static constexpr uint32_t kOffScale = kStages * kOperandBytes;
+  static constexpr uint32_t kOffBuf = kOffScale + kStages * kScaleBytes;
+  static constexpr uint32_t kOffBias = kOffBuf + kEpiWarps * kBufs * kBufBytes;
+  static constexpr uint32_t kOffBar = kOffBias + kEpiWarps * 32 * 4;
+  // barriers
+  static constexpr int kFull0 = 0;                     // leader: both CTAs' bytes landed
+  static constexpr int kEmpty0 = kStages;              // both: stage consumed
+  static constexpr int kAccFull0 = 2 * kStages;        // both: accumulator b complete
+  static constexpr int kAccEmpty0 = 2 * kStages + 2;   // leader: accumulator b drained by both
+  static constexpr int kDrain = 2 * kStages + 4;
+  static constexpr int kRes0 = 2 * kStages + 5;        // [warp][buf]: residual box landed
+  static constexpr int kNumBars = kRes0 + kEpiWarps * kBufs;
+  static constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;
+  static constexpr uint32_t kSmemBytes = kOffMisc + 16 + 1024;   // + alignment slack
+  static_assert(kOperandBytes % 1024 == 0 && kOffBuf % 512 == 0, "alignment");
+  static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+  static_assert(!MX || 2 * BN <= kScaleCols, "TMEM");
+};
+
+struct PairGrid {
+  int m_tiles, n_tiles, total, n_kb, k_steps, out_block_tiles, has_residual;
+};
+
+// Tile t: groups of kGroup row tiles; in a group, row tile fastest.
+__device__ __forceinline__ void decode(const PairGrid &g, int t, int &mt, int &nt) {
+  const int per = kGroup * g.n_tiles;
+  const int grp = t / per, r = t - grp * per;
+  const int left = g.m_tiles - grp * kGroup;
+  const int gm = left < kGroup ? left : kGroup;
+  nt = r / gm;
+  mt = grp * kGroup + (r - nt * gm);
+}
+
+template <bool MX, int BN, bool OUT8>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    linear_pair_kernel(const __grid_constant__ LinearParams p, const __grid_constant__ PairGrid g,
+                       const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw,
+                       const __grid_constant__ CUtensorMap tsx, const __grid_constant__ CUtensorMap tsw,
+                       const __grid_constant__ CUtensorMap tr, const __grid_constant__ CUtensorMap to) {
+  using S = Shape<MX, BN>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::kOffBar);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::kOffMisc);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + S::kOffMisc + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int pair = static_cast<int>(blockIdx.x >> 1), npairs = static_cast<int>(gridDim.x >> 1);
+
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    for (int b = 0; b < S::kNumBars; ++b)
+      mbar_init(bars + b, (b == S::kAccEmpty0 || b == S::kAccEmpty0 + 1) ? 2 * kEpiWarps : 1);
+    fence_barrier_init();
+  }
+  if (warp == kMmaWarp) {                   // same warp in both CTAs, same slot offset
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync();                           // barriers of both CTAs initialised, TMEM allocated
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const Ctx ctx{bars, abort_flag, p.status};
+
+  if (warp == kProducerWarp) {
+    // ------------------------------------------------------------ producer --
+    if (lane == 0) {
+      tma_prefetch_desc(&tx);
+      tma_prefetch_desc(&tw);
+      if constexpr (MX) {
+        tma_prefetch_desc(&tsx);
+        tma_prefetch_desc(&tsw);
+      }
+      int q = 0;                            // k-blocks issued by this CTA
+      bool ok = true;
+      for (int t = pair; ok && t < g.total; t += npairs) {
+        int mt, nt;
+        decode(g, t, mt, nt);
+        const int row0 = mt * 256 + static_cast<int>(rank) * 128;
+        const int col0 = nt * BN;
+        for (int kb = 0; kb < g.n_kb; ++kb, ++q) {
+          const int s = q % S::kStages;
+          if (!wait_bar(ctx, S::kEmpty0 + s, ((q / S::kStages) & 1) ^ 1)) {
+            ok = false;
+            break;
+          }
+          // The leader expects the bytes of both CTAs on its full barrier.
+          if (rank == 0) mbar_arrive_expect_tx(bars + S::kFull0 + s, 2 * S::kStageBytes);
+          uint8_t *sa = smem + s * S::kOperandBytes;
+          const uint32_t lb = leader_bar(bars + S::kFull0 + s);
+          tma_load_2d_pair(sa, &tx, lb, kb * S::kKElems, row0);
+          tma_load_2d_pair(sa + kABytes, &tw, lb, kb * S::kKElems, col0 + static_cast<int>(rank) * (BN / 2));
+          if constexpr (MX) {
+            uint8_t *ss = smem + S::kOffScale + s * S::kScaleBytes;
+            tma_load_3d_pair(ss, &tsx, lb, 0, kb, row0 >> 7);
+            tma_load_3d_pair(ss + 512, &tsw, lb, 0, kb, col0 >> 7);
+          }
+        }
+      }
+      // Tail: every stage this CTA filled has been consumed by the MMAs, so no
+      // load of this CTA is in flight when it exits.
+      for (int s = 0; s < S::kStages && q > 0; ++s) {
+        const int fills = q / S::kStages + (s < q % S::kStages ? 1 : 0);
+        if (fills > 0) drain_wait(ctx, S::kEmpty0 + s, (fills - 1) & 1);
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    // ---------------------------------------------------------- MMA issuer --
+    if (lane == 0 && rank == 0) {
+      const uint32_t hi = desc_hi_sw128(1024);
+      const uint32_t lo0 = desc_lo_sw128(smem_u32(smem), 16);
+      const uint32_t sc0 = smem_u32(smem + S::kOffScale);
+      int q = 0, i = 0;
+      bool ok = true;
+      for (int t = pair; ok && t < g.total; t += npairs, ++i) {
+        int mt, nt;
+        decode(g, t, mt, nt);
+        const int b = i & 1;
+        if (!wait_bar_cluster(ctx, S::kAccEmpty0 + b, ((i >> 1) & 1) ^ 1)) break;
+        tc_fence_after();
+        // BN = 192: odd feature tiles start at row 64 of a 128-row scale tile.
+        const uint32_t shift = (nt * BN & 127) >> 5;
+        for (int kb = 0; kb < g.n_kb; ++kb, ++q) {
+          const int s = q % S::kStages;
+          if (!wait_bar_cluster(ctx, S::kFull0 + s, (q / S::kStages) & 1)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a_lo = lo0 + ((s * S::kOperandBytes) >> 4);
+          const uint32_t b_lo = a_lo + (kABytes >> 4);
+          const int left = g.k_steps - kb * (S::kKElems / S::kKStep);
+          if constexpr (MX) {
+            const uint32_t sc = sc0 + s * S::kScaleBytes;
+            const uint32_t sfa = tmem + kScaleCols + 16 * (q & 3);
+            const uint32_t sfb = sfa + 4;
+            tmem_copy_scales_pair(sfa, make_desc_scale_tile(sc));
+            tmem_copy_scales_pair(sfb, make_desc_scale_tile(sc + 512));
+            tmem_copy_scales_pair(sfb + 4, make_desc_scale_tile(sc + 1024));
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (k < left)
+                mma_mx_ss2_pair(tmem + BN * b, a_lo + k * 2, b_lo + k * 2, hi,
+                                make_idesc_mx_e4m3(256, BN, k), sfa, sfb + shift,
+                                (kb > 0 || k > 0) ? 1u : 0u);
+          } else {
+            constexpr uint32_t idesc = make_idesc_bf16(256, BN, false);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (k < left)
+                mma_bf16_ss2_pair(tmem + BN * b, a_lo + k * 2, b_lo + k * 2, hi, idesc,
+                                  (kb > 0 || k > 0) ? 1u : 0u);
+          }
+          mma_commit_pair(bars + S::kEmpty0 + s);
+        }
+        if (ok) mma_commit_pair(bars + S::kAccFull0 + b);
+      }
+      // Drain: all MMAs issued by this thread complete before TMEM is freed.
+      mma_commit_pair(bars + S::kDrain);
+      drain_wait(ctx, S::kDrain, 0);
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue --
+    constexpr int kSteps = BN / 64;                      // 32-column steps of a warpgroup
+    const int e = warp >> 2;                             // column half of the tile
+    const int wr = (warp & 3) * 32;                      // first row of this warp
+    const uint32_t lane_addr = static_cast<uint32_t>(wr) << 16;
+    uint8_t *bufs = smem + S::kOffBuf + warp * kBufs * kBufBytes;
+    float *bias_row = reinterpret_cast<float *>(smem + S::kOffBias) + warp * 32;
+    const int res_bar = S::kRes0 + warp * kBufs;
+    uint32_t res_phase = 0;                              // bit per buffer
+    uint32_t res_pending = 0;                            // lane 0: boxes in flight
+    // First row and column of a step of a tile; false: wholly outside out.
+    auto place = [&](int t, int c, int &row0, int &col0) {
+      int mt, nt;
+      decode(g, t, mt, nt);
+      row0 = mt * 256 + static_cast<int>(rank) * 128 + wr;
+      col0 = nt * BN + e * (BN / 2) + c * 32;
+      return row0 < p.M && col0 < p.N;
+    };
+    auto fetch = [&](int t, int c, int buf) {            // lane 0: residual box of a step
+      int row0, col0;
+      if (t < g.total && place(t, c, row0, col0)) {
+        res_pending |= 1u << buf;
+        mbar_arrive_expect_tx(bars + res_bar + buf, kBufBytes);
+        tma_load_2d(bufs + buf * kBufBytes, &tr, bars + res_bar + buf, col0, row0);
+      }
+    };
+    auto bias_at = [&](int t, int c) {                   // this lane's column of a step
+      int row0, col0;
+      if (!p.bias || t >= g.total) return 0.f;
+      place(t, c, row0, col0);
+      return col0 + lane < p.N ? __ldg(p.bias + col0 + lane) : 0.f;
+    };
+    int buf = 0;
+    if (g.has_residual && lane == 0) fetch(pair, 0, 0);
+    float bias = bias_at(pair, 0);
+    bool ok = true;
+    int i = 0;
+    for (int t = pair; ok && t < g.total; t += npairs, ++i) {
+      const int b = i & 1;
+      ok = __all_sync(0xffffffffu, wait_bar_cluster(ctx, S::kAccFull0 + b, (i >> 1) & 1));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t tcol = tmem + lane_addr + BN * b + e * (BN / 2);
+      uint32_t cur[32], nxt[32];
+      tmem_ld32(tcol, cur);
+      tmem_ld_wait();
+      reg_fence32(cur);
+#pragma unroll
+      for (int c = 0; c < kSteps; ++c) {
+        if (c + 1 < kSteps) tmem_ld32(tcol + (c + 1) * 32, nxt);
+        int row0, col0;
+        const bool on = place(t, c, row0, col0);
+        const int t1 = c + 1 < kSteps ? t : t + npairs, c1 = c + 1 < kSteps ? c + 1 : 0;
+        const int buf1 = buf + 1 == kBufs ? 0 : buf + 1;
+        // Of this warp's stores at most the last one may still be reading its
+        // buffer: buf (three steps ago) and buf1 (two steps ago) are free.
+        if (lane == 0) {
+          asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+          if (g.has_residual) fetch(t1, c1, buf1);
+        }
+        bias_row[lane] = bias;
+        bias = bias_at(t1, c1);
+        __syncwarp();
+        if (on) {
+          float v[32];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float4 f = reinterpret_cast<const float4 *>(bias_row)[j];
+            v[4 * j] = __uint_as_float(cur[4 * j]) + f.x;
+            v[4 * j + 1] = __uint_as_float(cur[4 * j + 1]) + f.y;
+            v[4 * j + 2] = __uint_as_float(cur[4 * j + 2]) + f.z;
+            v[4 * j + 3] = __uint_as_float(cur[4 * j + 3]) + f.w;
+          }
+          if (p.act == kGelu) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = activate(v[j], kGelu);
+          } else if (p.act == kSilu) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = activate(v[j], kSilu);
+          }
+          uint8_t *stage = bufs + buf * kBufBytes;
+          if constexpr (OUT8) {
+            float m = 0.f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) m = fmaxf(m, fabsf(v[j]));
+            const int ex = block_exponent(m);
+            const float f = block_factor(ex);
+            const uint32_t addr = smem_u32(stage + lane * 32);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              uint32_t w[4];
+#pragma unroll
+              for (int h = 0; h < 4; ++h) {
+                const float *u = v + 16 * j + 4 * h;
+                w[h] = pack_e4m3x4(u[0] * f, u[1] * f, u[2] * f, u[3] * f);
+              }
+              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr + 16 * j),
+                           "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                           : "memory");
+            }
+            if (row0 + lane < p.M)
+              p.out.scales[scale_offset(row0 + lane, col0 >> 5, g.out_block_tiles)] =
+                  static_cast<uint8_t>(ex + 127);
+          } else {
+            // 64-byte rows, 64-byte swizzle: 16-byte chunk j of row r at j ^ (r / 2 % 4).
+            const uint32_t addr = smem_u32(stage + lane * 64);
+            const uint32_t x = (lane >> 1) & 3;
+            if (g.has_residual) {
+              ok = __all_sync(0xffffffffu, wait_bar(ctx, res_bar + buf, (res_phase >> buf) & 1));
+              if (!ok) break;
+              res_phase ^= 1u << buf;
+              res_pending &= ~(1u << buf);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                uint32_t w[4];
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                             : "r"(addr + ((j ^ x) << 4)));
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                  v[8 * j + 2 * h] += __uint_as_float(w[h] << 16);
+                  v[8 * j + 2 * h + 1] += __uint_as_float(w[h] & 0xffff0000u);
+                }
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t w[4];
+#pragma unroll
+              for (int h = 0; h < 4; ++h) {
+                const __nv_bfloat162 two = __floats2bfloat162_rn(v[8 * j + 2 * h], v[8 * j + 2 * h + 1]);
+                w[h] = *reinterpret_cast<const uint32_t *>(&two);
+              }
+              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr + ((j ^ x) << 4)),
+                           "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                           : "memory");
+            }
+          }
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) {
+          if (on) tma_store_2d(&to, bufs + buf * kBufBytes, col0, row0);
+          tma_store_commit();                            // a group per step, empty or not
+        }
+        buf = buf1;
+        if (c + 1 < kSteps) {
+          tmem_ld_wait();
+          reg_fence32(nxt);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) cur[j] = nxt[j];
+        }
+        if (c + 2 == kSteps) {
+          // Last TMEM load of this accumulator done: release it to the leader.
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(bars + S::kAccEmpty0 + b, 0);
+        }
+      }
+    }
+    if (lane == 0) {
+      // A fetch that no step took (another role gave up) must land before exit.
+      for (int k = 0; k < kBufs; ++k)
+        if (res_pending >> k & 1) drain_wait(ctx, res_bar + k, (res_phase >> k) & 1);
+      tma_store_wait_all();
+    }
+    __syncwarp();
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();                           // no MMA or load of the pair is in flight
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+template <bool MX, int BN, bool OUT8>
+cudaError_t run_pair(const LinearParams &p, cudaStream_t st) {
+  using S = Shape<MX, BN>;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const int elt = MX ? 1 : 2;
+  CUtensorMap tx{}, tw{}, tsx{}, tsw{}, tr{}, to{};
+  const uint64_t K = static_cast<uint64_t>(p.K), M = static_cast<uint64_t>(p.M), N = static_cast<uint64_t>(p.N);
+  const uint64_t xd[2] = {K, M}, wd[2] = {K, N}, od[2] = {N, M};
+  const uint64_t xs[1] = {static_cast<uint64_t>(p.x.ld) * elt}, ws[1] = {static_cast<uint64_t>(p.w.ld) * elt};
+  const uint32_t xb[2] = {S::kKElems, 128}, wb[2] = {S::kKElems, BN / 2}, ob[2] = {32, 32};
+  bool ok = encode_rows_map(&tx, elt, 128, p.x.data, 2, xd, xs, xb) &&
+            encode_rows_map(&tw, elt, 128, p.w.data, 2, wd, ws, wb);
+  if (MX) {
+    // Scale tiles as rows of 128 words: [row tiles][block tiles][128].
+    const uint64_t kt = (K + 127) / 128;
+    const uint64_t sd[3] = {128, kt, (M + 127) / 128}, qd[3] = {128, kt, (N + 127) / 128};
+    const uint64_t ss[2] = {512, 512 * kt};
+    const uint32_t sb[3] = {128, 1, 1}, qb[3] = {128, 1, 2};
+    ok = ok && encode_rows_map(&tsx, 4, 0, p.x.scales, 3, sd, ss, sb) &&
+         encode_rows_map(&tsw, 4, 0, p.w.scales, 3, qd, ss, qb);
+  }
+  const int oelt = OUT8 ? 1 : 2;
+  const uint64_t os[1] = {static_cast<uint64_t>(p.out.ld) * oelt};
+  ok = ok && encode_rows_map(&to, oelt, OUT8 ? 0 : 64, p.out.data, 2, od, os, ob);
+  if (p.residual.data) {
+    const uint64_t rs[1] = {static_cast<uint64_t>(p.residual.ld) * 2};
+    ok = ok && encode_rows_map(&tr, 2, 64, p.residual.data, 2, od, rs, ob);
+  }
+  if (!ok) return cudaErrorInvalidValue;
+  PairGrid g{};
+  const int64_t mt = (static_cast<int64_t>(p.M) + 255) / 256, nt = (static_cast<int64_t>(p.N) + BN - 1) / BN;
+  if (mt * nt > 0x7fffffff - 65536) return cudaErrorInvalidValue;
+  g.m_tiles = static_cast<int>(mt);
+  g.n_tiles = static_cast<int>(nt);
+  g.total = static_cast<int>(mt * nt);
+  g.n_kb = (p.K + S::kKElems - 1) / S::kKElems;
+  g.k_steps = (p.K + S::kKStep - 1) / S::kKStep;
+  g.out_block_tiles = (p.N + 127) / 128;
+  g.has_residual = p.residual.data != nullptr;
+  e = cudaFuncSetAttribute(linear_pair_kernel<MX, BN, OUT8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(S::kSmemBytes));
+  if (e != cudaSuccess) return e;
+  const int pairs = g.total < sms / 2 ? g.total : sms / 2;
+  linear_pair_kernel<MX, BN, OUT8><<<2 * pairs, kThreads, S::kSmemBytes, st>>>(p, g, tx, tw, tsx, tsw, tr, to);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_linear_pair(const LinearParams &p, bool e4m3, bool out_e4m3, int bn, cudaStream_t st) {
+  if (e4m3) return out_e4m3 ? run_pair<true, 192, true>(p, st) : run_pair<true, 192, false>(p, st);
+  if (bn == 256) return out_e4m3 ? run_pair<false, 256, true>(p, st) : run_pair<false, 256, false>(p, st);
+  return out_e4m3 ? run_pair<false, 192, true>(p, st) : run_pair<false, 192, false>(p, st);
+}
+
+}  // namespace wf

@@ -330,6 +330,33 @@ bool on_pool_device(const wf_pool *p) {
 
 }  // namespace
 
+namespace wf {
+
+bool encode_rows_map(void *map, int elt, int swizzle, const void *base, int rank,
+                     const uint64_t *dims, const uint64_t *strides_bytes, const uint32_t *box) {
+  auto fn = get_encode();
+  if (!fn) return false;
+  const CUtensorMapDataType type = elt == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : elt == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                              : CU_TENSOR_MAP_DATA_TYPE_UINT32;
+  const CUtensorMapSwizzle sw = swizzle == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                                : swizzle == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                : swizzle == 32 ? CU_TENSOR_MAP_SWIZZLE_32B
+                                                : CU_TENSOR_MAP_SWIZZLE_NONE;
+  cuuint64_t d[5], s[5];
+  cuuint32_t b[5], one[5] = {1, 1, 1, 1, 1};
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    b[i] = box[i];
+    if (i + 1 < rank) s[i] = strides_bytes[i];
+  }
+  return fn(static_cast<CUtensorMap *>(map), type, rank, const_cast<void *>(base), d, s, b, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace wf
+
 extern "C" {
 
 const char *wf_status_string(wf_status s) {

@@ -1,0 +1,256 @@
+// Host side of the row operators: checks of arguments and choice of kernel.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "rows.cuh"
+#include "wf.h"
+#include "wf_internal.h"
+
+namespace wf {
+namespace {
+
+constexpr int64_t kMaxDim = 0x7fffff00;        // row and column numbers of any tile fit int32
+constexpr int64_t kMaxLd = int64_t(1) << 37;   // keeps a row stride within a tensor map's 2^40 bytes
+
+int element_size(int32_t dtype) {
+  return dtype == WF_DTYPE_F32 ? 4 : dtype == WF_DTYPE_BF16 ? 2 : 1;
+}
+
+bool multiple_of(const void *p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+wf_status check_rows(const wf_rows *r) {
+  if (!r) return WF_ERR_INVALID_ARG;
+  if (r->dtype != WF_DTYPE_BF16 && r->dtype != WF_DTYPE_F32 && r->dtype != WF_DTYPE_FP8_E4M3)
+    return WF_ERR_INVALID_ARG;
+  if (r->rows < 0 || r->rows > kMaxDim || r->cols < 1 || r->cols > kMaxDim || r->ld < r->cols ||
+      r->ld > kMaxLd)
+    return WF_ERR_INVALID_ARG;
+  if (r->rows > (int64_t(1) << 60) / (r->ld * element_size(r->dtype))) return WF_ERR_INVALID_ARG;
+  if (r->dtype == WF_DTYPE_FP8_E4M3 && (r->cols % 32 != 0 || r->ld % 16 != 0)) return WF_ERR_INVALID_ARG;
+  if (r->rows == 0) return WF_OK;              // empty rows may have no memory
+  if (!r->data || !multiple_of(r->data, element_size(r->dtype))) return WF_ERR_INVALID_ARG;
+  if (r->dtype == WF_DTYPE_FP8_E4M3 &&
+      (!multiple_of(r->data, 16) || !r->scales || !multiple_of(r->scales, 16)))
+    return WF_ERR_INVALID_ARG;
+  return WF_OK;
+}
+
+bool same_shape(const wf_rows *a, const wf_rows *b) { return a->rows == b->rows && a->cols == b->cols; }
+
+// The bytes that an operand touches: `count` pieces of `width` bytes, `pitch`
+// bytes from one to the next.
+struct Span {
+  uintptr_t base;
+  int64_t width, pitch, count;
+};
+
+Span data_span(const wf_rows *r) {
+  const int64_t elt = element_size(r->dtype);
+  return {reinterpret_cast<uintptr_t>(r->data), r->cols * elt, r->ld * elt, r->rows};
+}
+
+Span scale_span(const wf_rows *r) {
+  const int64_t n = (r->rows + 127) / 128 * ((r->cols + 127) / 128) * 512;
+  return {reinterpret_cast<uintptr_t>(r->scales), n, n, 1};
+}
+
+Span vector_span(const float *v, int64_t n) { return {reinterpret_cast<uintptr_t>(v), 4 * n, 4 * n, 1}; }
+
+// Whether two spans share a byte. Two column ranges of one strided buffer do
+// not; spans of different pitches are taken as overlapping if their ranges do.
+bool overlap(const Span &a, const Span &b) {
+  if (a.count == 0 || b.count == 0 || !a.base || !b.base) return false;
+  const uintptr_t ae = a.base + (a.count - 1) * a.pitch + a.width, be = b.base + (b.count - 1) * b.pitch + b.width;
+  if (ae <= b.base || be <= a.base) return false;
+  if (a.pitch != b.pitch) return true;
+  const int64_t off = static_cast<int64_t>((b.base - a.base) % static_cast<uint64_t>(a.pitch));
+  const int64_t d = b.base >= a.base ? off
+                                     : (a.pitch - static_cast<int64_t>((a.base - b.base) % static_cast<uint64_t>(a.pitch))) % a.pitch;
+  return d < a.width || d + b.width > a.pitch;
+}
+
+bool same_place(const wf_rows *a, const wf_rows *b) {
+  return a->data == b->data && a->ld == b->ld && a->dtype == b->dtype;
+}
+
+// Whether an output collides with an input or another output. `in_place`: the
+// output may be exactly that operand.
+bool collides(const wf_rows *out, const wf_rows *other, bool in_place) {
+  if (!other) return false;
+  if (in_place && same_place(out, other)) return false;
+  const Span od = data_span(out), xd = data_span(other);
+  if (overlap(od, xd)) return true;
+  const bool os = out->dtype == WF_DTYPE_FP8_E4M3, xs = other->dtype == WF_DTYPE_FP8_E4M3;
+  if (os && overlap(scale_span(out), xd)) return true;
+  if (xs && overlap(od, scale_span(other))) return true;
+  return os && xs && overlap(scale_span(out), scale_span(other));
+}
+
+bool collides(const wf_rows *out, const float *v, int64_t n) {
+  if (!v) return false;
+  const Span s = vector_span(v, n);
+  return overlap(data_span(out), s) || (out->dtype == WF_DTYPE_FP8_E4M3 && overlap(scale_span(out), s));
+}
+
+// An E4M3 output's codes and scales must be apart too.
+bool folded(const wf_rows *out) {
+  return out->dtype == WF_DTYPE_FP8_E4M3 && overlap(data_span(out), scale_span(out));
+}
+
+// The stride of a single row is never used, so it is taken as one that suits
+// every access: the next multiple of 16 elements.
+int64_t row_stride(const wf_rows *r) { return r->rows == 1 ? (r->cols + 15) / 16 * 16 : r->ld; }
+
+RowsView view(const wf_rows *r) {
+  if (!r) return {nullptr, nullptr, 0};
+  return {r->data, static_cast<uint8_t *>(r->scales), row_stride(r)};
+}
+
+RowsType type_of(int32_t dtype) {
+  return dtype == WF_DTYPE_BF16 ? RowsType::kBf16 : dtype == WF_DTYPE_F32 ? RowsType::kF32 : RowsType::kE4m3;
+}
+
+wf_status status_of(cudaError_t e) { return e == cudaSuccess ? WF_OK : WF_ERR_CUDA; }
+
+wf_status convert(const wf_rows *x, const wf_rows *out, bool to_e4m3, cudaStream_t st) {
+  wf_status s = check_rows(x);
+  if (s == WF_OK) s = check_rows(out);
+  if (s != WF_OK) return s;
+  const wf_rows *wide = to_e4m3 ? x : out, *codes = to_e4m3 ? out : x;
+  if (wide->dtype == WF_DTYPE_FP8_E4M3 || codes->dtype != WF_DTYPE_FP8_E4M3) return WF_ERR_INVALID_ARG;
+  if (!same_shape(x, out)) return WF_ERR_INVALID_ARG;
+  if (x->rows == 0) return WF_OK;
+  if (x->rows * (x->cols / 16) > kMaxDim) return WF_ERR_UNSUPPORTED;   // 32-bit indexes
+  if (collides(out, x, false) || folded(out)) return WF_ERR_INVALID_ARG;
+  ConvertParams p{};
+  p.x = view(x);
+  p.out = view(out);
+  p.rows = static_cast<int32_t>(x->rows);
+  p.cols = static_cast<int32_t>(x->cols);
+  return status_of(to_e4m3 ? launch_quantize_rows(p, type_of(x->dtype), st)
+                           : launch_dequantize_rows(p, type_of(out->dtype), st));
+}
+
+bool rows16(const wf_rows *r) {
+  return multiple_of(r->data, 16) && row_stride(r) * element_size(r->dtype) % 16 == 0;
+}
+
+}  // namespace
+}  // namespace wf
+
+using namespace wf;
+
+extern "C" {
+
+wf_status wf_scale_bytes(int64_t rows, int64_t cols, size_t *bytes) {
+  if (!bytes || rows < 0 || rows > kMaxDim || cols < 1 || cols > kMaxDim || cols % 32 != 0)
+    return WF_ERR_INVALID_ARG;
+  *bytes = static_cast<size_t>((rows + 127) / 128) * static_cast<size_t>((cols + 127) / 128) * 512;
+  return WF_OK;
+}
+
+wf_status wf_quantize_rows(const wf_rows *x, const wf_rows *out, wf_stream_t stream) {
+  return convert(x, out, true, reinterpret_cast<cudaStream_t>(stream));
+}
+
+wf_status wf_dequantize_rows(const wf_rows *x, const wf_rows *out, wf_stream_t stream) {
+  return convert(x, out, false, reinterpret_cast<cudaStream_t>(stream));
+}
+
+wf_status wf_add_rms_norm(const wf_rows *x, const wf_rows *residual, const float *weight, float eps,
+                          const wf_rows *sum, const wf_rows *out, wf_stream_t stream) {
+  wf_status s = check_rows(x);
+  if (s == WF_OK && residual) s = check_rows(residual);
+  if (s == WF_OK && sum) s = check_rows(sum);
+  if (s == WF_OK) s = check_rows(out);
+  if (s != WF_OK) return s;
+  if (x->dtype == WF_DTYPE_FP8_E4M3) return WF_ERR_INVALID_ARG;
+  if (residual && (residual->dtype != x->dtype || !same_shape(x, residual))) return WF_ERR_INVALID_ARG;
+  if (sum && (sum->dtype != x->dtype || !same_shape(x, sum))) return WF_ERR_INVALID_ARG;
+  if ((out->dtype != x->dtype && out->dtype != WF_DTYPE_FP8_E4M3) || !same_shape(x, out))
+    return WF_ERR_INVALID_ARG;
+  if (!(eps >= 0.0f) || !std::isfinite(eps) || !multiple_of(weight, 4)) return WF_ERR_INVALID_ARG;
+  if (x->rows == 0) return WF_OK;
+  if (collides(out, x, true) || collides(out, residual, true) || collides(out, sum, false) ||
+      collides(out, weight, x->cols) || folded(out))
+    return WF_ERR_INVALID_ARG;
+  if (sum && (collides(sum, x, true) || collides(sum, residual, true) || collides(sum, weight, x->cols)))
+    return WF_ERR_INVALID_ARG;
+  NormParams p{};
+  p.x = view(x);
+  p.residual = view(residual);
+  p.sum = view(sum);
+  p.out = view(out);
+  p.weight = weight;
+  p.eps = eps;
+  p.rows = static_cast<int32_t>(x->rows);
+  p.cols = static_cast<int32_t>(x->cols);
+  return status_of(launch_add_rms_norm(p, type_of(x->dtype), out->dtype == WF_DTYPE_FP8_E4M3,
+                                       reinterpret_cast<cudaStream_t>(stream)));
+}
+
+wf_status wf_linear(const wf_rows *x, const wf_rows *w, const float *bias, int32_t act,
+                    const wf_rows *residual, const wf_rows *out, wf_stream_t stream) {
+  wf_status s = check_rows(x);
+  if (s == WF_OK) s = check_rows(w);
+  if (s == WF_OK && residual) s = check_rows(residual);
+  if (s == WF_OK) s = check_rows(out);
+  if (s != WF_OK) return s;
+  if (act != WF_ACT_NONE && act != WF_ACT_GELU && act != WF_ACT_SILU) return WF_ERR_INVALID_ARG;
+  if (x->cols != w->cols || out->rows != x->rows || out->cols != w->rows) return WF_ERR_INVALID_ARG;
+  if (residual && !same_shape(residual, out)) return WF_ERR_INVALID_ARG;
+  if (x->dtype == WF_DTYPE_F32 || w->dtype != x->dtype || out->dtype == WF_DTYPE_F32) return WF_ERR_UNSUPPORTED;
+  if (residual && (residual->dtype != WF_DTYPE_BF16 || out->dtype != WF_DTYPE_BF16)) return WF_ERR_UNSUPPORTED;
+  if (!multiple_of(bias, 4)) return WF_ERR_INVALID_ARG;
+  if (x->rows == 0) return WF_OK;
+  if (!rows16(x) || !rows16(w)) return WF_ERR_INVALID_ARG;
+  if (collides(out, x, false) || collides(out, w, false) || collides(out, residual, true) ||
+      collides(out, bias, out->cols) || folded(out))
+    return WF_ERR_INVALID_ARG;
+  const bool e4m3 = x->dtype == WF_DTYPE_FP8_E4M3, out8 = out->dtype == WF_DTYPE_FP8_E4M3;
+  LinearParams p{};
+  p.x = view(x);
+  p.w = view(w);
+  p.residual = view(residual);
+  p.out = view(out);
+  p.bias = bias;
+  p.act = act;
+  p.M = static_cast<int32_t>(x->rows);
+  p.N = static_cast<int32_t>(w->rows);
+  p.K = static_cast<int32_t>(x->cols);
+  if (rows_status_word(&p.status) != cudaSuccess) return WF_ERR_CUDA;
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool stored_by_tma = rows16(out) && (!residual || rows16(residual));
+  int sms = 0, dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return WF_ERR_CUDA;
+  const int64_t m_tiles = (x->rows + 255) / 256;
+  if (stored_by_tma && x->rows > 128 && m_tiles * ((w->rows + 191) / 192) >= sms / 4) {
+    // Waves of CTA pairs times the tile's width: what the last wave wastes.
+    const int64_t pairs = sms / 2;
+    const int64_t w192 = (m_tiles * ((w->rows + 191) / 192) + pairs - 1) / pairs * 192;
+    const int64_t w256 = (m_tiles * ((w->rows + 255) / 256) + pairs - 1) / pairs * 256;
+    return status_of(launch_linear_pair(p, e4m3, out8, w256 <= w192 ? 256 : 192, st));
+  }
+  const int nt = x->rows <= 16 ? 16 : x->rows <= 32 ? 32 : x->rows <= 64 ? 64 : 128;
+  const int64_t tiles = (w->rows + 127) / 128 * ((x->rows + nt - 1) / nt);
+  const int64_t n_kb = e4m3 ? (x->cols + 127) / 128 : (x->cols + 63) / 64;
+  int split = 1;
+  while (split < 8 && tiles * split < sms && n_kb >= 4 * split) split *= 2;
+  return status_of(launch_linear_skinny(p, e4m3, out8, nt, split, st));
+}
+
+wf_status wf_rows_check_status(wf_stream_t stream) {
+  if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return WF_ERR_CUDA;
+  int32_t *word = nullptr;
+  if (rows_status_word(&word) != cudaSuccess) return WF_ERR_CUDA;
+  int32_t v = 0;
+  if (cudaMemcpy(&v, word, 4, cudaMemcpyDeviceToHost) != cudaSuccess) return WF_ERR_CUDA;
+  if (v != 0 && cudaMemset(word, 0, 4) != cudaSuccess) return WF_ERR_CUDA;
+  return static_cast<wf_status>(v);
+}
+
+}  // extern "C"

@@ -1,0 +1,423 @@
+// Residual addition + root-mean-square norm, and E4M3 rows to and from bf16 or
+// fp32, for sm_100a.
+//
+// All three read each element once and write each result once; HBM bounds them.
+//
+// Norm: s = x + residual, out = s / sqrt(mean(s^2) + eps) * weight.
+//   A row stays in registers between its one read and its one write: 1, 2, 4 or
+//   8 warps share a row, each lane holds up to four chunks of 8 elements (16-byte
+//   loads of bf16), all of a row's loads are issued before the first use, and
+//   the weight's chunks stay in registers over the rows that a block walks. The
+//   sum of squares is fp32: per lane, then by shuffles, then over the row's warps
+//   through shared memory in a fixed order.
+//   E4M3 output: a block of 32 columns is four neighbouring lanes' chunks, so its
+//   largest magnitude takes two shuffles; the codes are made from the fp32
+//   values, not from their bf16 rounding.
+//   Rows that 16-byte loads cannot take (odd widths or strides) or that
+//   registers cannot hold (over 8192 columns) go through a block per row that
+//   reads the row twice (the second time mostly from L1/L2).
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "rows.cuh"
+#include "sm100.cuh"
+
+namespace wf {
+namespace {
+
+using sm100::pack_e4m3x4;
+
+constexpr int kNormThreads = 256;
+
+// Eight consecutive elements as fp32; 16-byte aligned.
+struct Raw16 { uint4 a; };
+struct Raw32 { float4 a, b; };
+template <typename T> struct RawOf;
+template <> struct RawOf<__nv_bfloat16> { using type = Raw16; };
+template <> struct RawOf<float> { using type = Raw32; };
+
+__device__ __forceinline__ Raw16 load8(const __nv_bfloat16 *p) {
+  return {__ldcs(reinterpret_cast<const uint4 *>(p))};
+}
+__device__ __forceinline__ Raw32 load8(const float *p) {
+  return {__ldcs(reinterpret_cast<const float4 *>(p)), __ldcs(reinterpret_cast<const float4 *>(p) + 1)};
+}
+__device__ __forceinline__ void widen8(const Raw16 &r, float (&v)[8]) {
+  const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void widen8(const Raw32 &r, float (&v)[8]) {
+  v[0] = r.a.x; v[1] = r.a.y; v[2] = r.a.z; v[3] = r.a.w;
+  v[4] = r.b.x; v[5] = r.b.y; v[6] = r.b.z; v[7] = r.b.w;
+}
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t *>(&b);
+  }
+  *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
+  *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  *(reinterpret_cast<float4 *>(p) + 1) = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ float widen(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float widen(float v) { return v; }
+__device__ __forceinline__ void narrow(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void narrow(float *p, float v) { *p = v; }
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Largest magnitude; fmaxf leaves NaN out.
+__device__ __forceinline__ float amax8(const float (&v)[8]) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
+  return m;
+}
+
+// WPR warps per row, CH chunks of 8 elements per lane.
+template <typename T, bool OUT8, int WPR, int CH>
+__global__ void __launch_bounds__(kNormThreads)
+    norm_kernel(const NormParams p) {
+  constexpr int kRows = kNormThreads / 32 / WPR;   // rows per block and pass
+  __shared__ float part[2][kNormThreads / 32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sub = warp / WPR;                      // row of the block's pass
+  const int t = (warp % WPR) * 32 + lane;          // thread of the row
+  const int chunks = p.cols >> 3;
+  const float inv = 1.0f / static_cast<float>(p.cols);
+  float w[CH][8];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int k = t + c * 32 * WPR;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[c][i] = 1.0f;
+    if (p.weight && k < chunks) {
+      const float4 a = __ldg(reinterpret_cast<const float4 *>(p.weight) + 2 * k);
+      const float4 b = __ldg(reinterpret_cast<const float4 *>(p.weight) + 2 * k + 1);
+      w[c][0] = a.x; w[c][1] = a.y; w[c][2] = a.z; w[c][3] = a.w;
+      w[c][4] = b.x; w[c][5] = b.y; w[c][6] = b.z; w[c][7] = b.w;
+    }
+  }
+  const int block_tiles = (p.cols + 127) >> 7;
+  int turn = 0;
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * kRows; base < p.rows;
+       base += static_cast<int64_t>(gridDim.x) * kRows, turn ^= 1) {
+    const int64_t row = base + sub;
+    const bool live = row < p.rows;
+    const T *x = static_cast<const T *>(p.x.data) + row * p.x.ld;
+    const T *r = p.residual.data ? static_cast<const T *>(p.residual.data) + row * p.residual.ld : nullptr;
+    typename RawOf<T>::type rx[CH], rr[CH];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int k = t + c * 32 * WPR;
+      if (live && k < chunks) {
+        rx[c] = load8(x + 8 * k);
+        if (r) rr[c] = load8(r + 8 * k);
+      }
+    }
+    float v[CH][8];
+    float ss = 0.f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const bool on = live && t + c * 32 * WPR < chunks;
+      if (on) {
+        widen8(rx[c], v[c]);
+        if (r) {
+          float u[8];
+          widen8(rr[c], u);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[c][i] += u[i];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[c][i] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = fmaf(v[c][i], v[c][i], ss);
+    }
+    ss = warp_sum(ss);
+    if constexpr (WPR > 1) {
+      // Two sets of partial sums in turn, so one barrier per pass is enough.
+      if (lane == 0) part[turn][warp] = ss;
+      __syncthreads();
+      ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < WPR; ++i) ss += part[turn][sub * WPR + i];
+    }
+    const float scale = 1.0f / sqrtf(ss * inv + p.eps);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int k = t + c * 32 * WPR;
+      const bool on = live && k < chunks;
+      if (on && p.sum.data) store8(static_cast<T *>(p.sum.data) + row * p.sum.ld + 8 * k, v[c]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[c][i] = v[c][i] * scale * w[c][i];
+      if constexpr (OUT8) {
+        float m = amax8(v[c]);
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        const int e = block_exponent(m);
+        const float f = block_factor(e);
+        if (on) {
+          const uint2 codes = make_uint2(
+              pack_e4m3x4(v[c][0] * f, v[c][1] * f, v[c][2] * f, v[c][3] * f),
+              pack_e4m3x4(v[c][4] * f, v[c][5] * f, v[c][6] * f, v[c][7] * f));
+          *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.out.data) + row * p.out.ld + 8 * k) = codes;
+          if ((k & 3) == 0)
+            p.out.scales[scale_offset(row, k >> 2, block_tiles)] = static_cast<uint8_t>(e + 127);
+        }
+      } else if (on) {
+        store8(static_cast<T *>(p.out.data) + row * p.out.ld + 8 * k, v[c]);
+      }
+    }
+  }
+}
+
+// Any width, alignment and stride: one block per row, the row read twice. A
+// thread's elements are the same in both readings, so outputs may be the inputs.
+template <typename T, bool OUT8>
+__global__ void __launch_bounds__(kNormThreads) norm_any_kernel(const NormParams p) {
+  __shared__ float part[2][kNormThreads / 32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const float inv = 1.0f / static_cast<float>(p.cols);
+  const int block_tiles = (p.cols + 127) >> 7;
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
+    const T *x = static_cast<const T *>(p.x.data) + row * p.x.ld;
+    const T *r = p.residual.data ? static_cast<const T *>(p.residual.data) + row * p.residual.ld : nullptr;
+    float ss = 0.f;
+    for (int64_t k = threadIdx.x; k < p.cols; k += kNormThreads) {
+      const float v = widen(x[k]) + (r ? widen(r[k]) : 0.f);
+      ss = fmaf(v, v, ss);
+    }
+    ss = warp_sum(ss);
+    if (lane == 0) part[turn][warp] = ss;
+    __syncthreads();
+    ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < kNormThreads / 32; ++i) ss += part[turn][i];
+    const float scale = 1.0f / sqrtf(ss * inv + p.eps);
+    // cols is a multiple of 32 for E4M3, so a warp is wholly in or out there.
+    for (int64_t k = threadIdx.x; k < p.cols; k += kNormThreads) {
+      const float s = widen(x[k]) + (r ? widen(r[k]) : 0.f);
+      const float v = s * scale * (p.weight ? __ldg(p.weight + k) : 1.0f);
+      if (p.sum.data) narrow(static_cast<T *>(p.sum.data) + row * p.sum.ld + k, s);
+      if constexpr (OUT8) {
+        const float a = fabsf(v);
+        const uint32_t m = __reduce_max_sync(0xffffffffu, a == a ? __float_as_uint(a) : 0u);
+        const int e = block_exponent(__uint_as_float(m));
+        static_cast<uint8_t *>(p.out.data)[row * p.out.ld + k] =
+            static_cast<uint8_t>(sm100::pack_e4m3x2(v * block_factor(e), 0.f) & 0xffu);
+        if (lane == 0)
+          p.out.scales[scale_offset(row, static_cast<int>(k >> 5), block_tiles)] = static_cast<uint8_t>(e + 127);
+      } else {
+        narrow(static_cast<T *>(p.out.data) + row * p.out.ld + k, v);
+      }
+    }
+  }
+}
+
+// Rows to E4M3: 16 columns per thread, a block of 32 is two neighbouring lanes.
+// VEC: 16-byte loads; else element by element.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) quantize_kernel(const ConvertParams p) {
+  const uint32_t per_row = static_cast<uint32_t>(p.cols) >> 4;
+  const uint32_t total = static_cast<uint32_t>(p.rows) * per_row;   // even, < 2^31 (host check)
+  const int block_tiles = (p.cols + 127) >> 7;
+  for (uint32_t i = blockIdx.x * 256u + threadIdx.x; i < total; i += gridDim.x * 256u) {
+    const uint32_t row = i / per_row, k = i - row * per_row;
+    const T *x = static_cast<const T *>(p.x.data) + static_cast<int64_t>(row) * p.x.ld + 16 * k;
+    float v[2][8];
+    if constexpr (VEC) {
+      const auto a = load8(x), b = load8(x + 8);
+      widen8(a, v[0]);
+      widen8(b, v[1]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j >> 3][j & 7] = widen(x[j]);
+    }
+    float m = fmaxf(amax8(v[0]), amax8(v[1]));
+    // The pair's other lane is in the loop too: total is even.
+    const uint32_t pair = 3u << (threadIdx.x & 30);
+    m = fmaxf(m, __shfl_xor_sync(pair, m, 1));
+    const int e = block_exponent(m);
+    const float f = block_factor(e);
+    uint32_t c[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float *u = v[j >> 1] + 4 * (j & 1);
+      c[j] = pack_e4m3x4(u[0] * f, u[1] * f, u[2] * f, u[3] * f);
+    }
+    *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out.data) + static_cast<int64_t>(row) * p.out.ld + 16 * k) =
+        make_uint4(c[0], c[1], c[2], c[3]);
+    if ((k & 1) == 0)
+      p.out.scales[scale_offset(row, static_cast<int>(k >> 1), block_tiles)] = static_cast<uint8_t>(e + 127);
+  }
+}
+
+// E4M3 rows to T: 16 columns per thread. The product with 2^e is exact in fp32.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) dequantize_kernel(const ConvertParams p) {
+  const uint32_t per_row = static_cast<uint32_t>(p.cols) >> 4;
+  const uint32_t total = static_cast<uint32_t>(p.rows) * per_row;
+  const int block_tiles = (p.cols + 127) >> 7;
+  for (uint32_t i = blockIdx.x * 256u + threadIdx.x; i < total; i += gridDim.x * 256u) {
+    const uint32_t row = i / per_row, k = i - row * per_row;
+    const uint4 c = *reinterpret_cast<const uint4 *>(
+        static_cast<const uint8_t *>(p.x.data) + static_cast<int64_t>(row) * p.x.ld + 16 * k);
+    const int s = p.x.scales[scale_offset(row, static_cast<int>(k >> 1), block_tiles)];
+    // 2^(s - 127) as two factors, so that the ends of the byte's range are exact too.
+    const float f0 = __uint_as_float(static_cast<uint32_t>((s >> 1) + 64) << 23);
+    const float f1 = __uint_as_float(static_cast<uint32_t>(s - (s >> 1) + 63) << 23);
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+    float v[2][8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+          static_cast<__nv_fp8x2_storage_t>(w[j >> 1] >> (16 * (j & 1))), __NV_E4M3);
+      const float2 f = __half22float2(__half2(h));
+      v[j >> 2][2 * (j & 3)] = f.x * f0 * f1;
+      v[j >> 2][2 * (j & 3) + 1] = f.y * f0 * f1;
+    }
+    T *out = static_cast<T *>(p.out.data) + static_cast<int64_t>(row) * p.out.ld + 16 * k;
+    if constexpr (VEC) {
+      store8(out, v[0]);
+      store8(out + 8, v[1]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) narrow(out + j, v[j >> 3][j & 7]);
+    }
+  }
+}
+
+bool aligned(const void *p, int64_t ld, int64_t elt) {
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (ld * elt) % 16 == 0;
+}
+
+cudaError_t sm_count(int *sms) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  return e;
+}
+
+// Blocks that the device holds at once: a grid of that size walks the rows with
+// the weight in registers and no second wave.
+template <typename K>
+cudaError_t resident_blocks(K kernel, int threads, int sms, int64_t *blocks) {
+  int per_sm = 0;
+  const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, 0);
+  *blocks = static_cast<int64_t>(per_sm > 0 ? per_sm : 1) * sms;
+  return e;
+}
+
+template <typename T, bool OUT8, int WPR, int CH>
+cudaError_t run_norm(const NormParams &p, int sms, cudaStream_t st) {
+  constexpr int kRows = kNormThreads / 32 / WPR;
+  int64_t grid = 0;
+  const cudaError_t e = resident_blocks(norm_kernel<T, OUT8, WPR, CH>, kNormThreads, sms, &grid);
+  if (e != cudaSuccess) return e;
+  const int64_t need = (p.rows + kRows - 1) / kRows;
+  norm_kernel<T, OUT8, WPR, CH><<<static_cast<unsigned>(need < grid ? need : grid), kNormThreads, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+template <typename T, bool OUT8>
+cudaError_t pick_norm(const NormParams &p, cudaStream_t st) {
+  int sms = 0;
+  const cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  const int64_t elt = sizeof(T);
+  const bool vec = p.cols % 8 == 0 && p.cols <= 8192 && aligned(p.x.data, p.x.ld, elt) &&
+                   (!p.residual.data || aligned(p.residual.data, p.residual.ld, elt)) &&
+                   (!p.sum.data || aligned(p.sum.data, p.sum.ld, elt)) &&
+                   aligned(p.out.data, p.out.ld, OUT8 ? 1 : elt) &&
+                   (reinterpret_cast<uintptr_t>(p.weight) & 15u) == 0;
+  if (!vec) {
+    const int64_t grid = static_cast<int64_t>(sms) * 8;
+    norm_any_kernel<T, OUT8><<<static_cast<unsigned>(p.rows < grid ? p.rows : grid), kNormThreads, 0, st>>>(p);
+    return cudaGetLastError();
+  }
+  // Fewest warps per row that keep it at three chunks a lane (24 fp32 values,
+  // as many weights, and the raw loads in flight).
+  const int per_warp = (p.cols + 255) / 256;         // chunks per lane with one warp
+  if (per_warp <= 1) return run_norm<T, OUT8, 1, 1>(p, sms, st);
+  if (per_warp <= 2) return run_norm<T, OUT8, 1, 2>(p, sms, st);
+  if (per_warp <= 3) return run_norm<T, OUT8, 1, 3>(p, sms, st);
+  if (per_warp <= 4) return run_norm<T, OUT8, 2, 2>(p, sms, st);
+  if (per_warp <= 6) return run_norm<T, OUT8, 2, 3>(p, sms, st);
+  if (per_warp <= 8) return run_norm<T, OUT8, 4, 2>(p, sms, st);
+  if (per_warp <= 12) return run_norm<T, OUT8, 4, 3>(p, sms, st);
+  if (per_warp <= 16) return run_norm<T, OUT8, 8, 2>(p, sms, st);
+  if (per_warp <= 24) return run_norm<T, OUT8, 8, 3>(p, sms, st);
+  return run_norm<T, OUT8, 8, 4>(p, sms, st);
+}
+
+unsigned convert_grid(const ConvertParams &p, int sms) {
+  const int64_t need = (static_cast<int64_t>(p.rows) * (p.cols / 16) + 255) / 256;
+  const int64_t most = static_cast<int64_t>(sms) * 64;
+  return static_cast<unsigned>(need < most ? need : most);
+}
+
+}  // namespace
+
+// Sticky status of the row operators that wait on barriers: one word per device.
+__device__ int32_t g_rows_status;
+
+cudaError_t rows_status_word(int32_t **word) {
+  void *p = nullptr;
+  const cudaError_t e = cudaGetSymbolAddress(&p, g_rows_status);
+  *word = static_cast<int32_t *>(p);
+  return e;
+}
+
+cudaError_t launch_add_rms_norm(const NormParams &p, RowsType in, bool out_e4m3, cudaStream_t st) {
+  if (in == RowsType::kBf16)
+    return out_e4m3 ? pick_norm<__nv_bfloat16, true>(p, st) : pick_norm<__nv_bfloat16, false>(p, st);
+  return out_e4m3 ? pick_norm<float, true>(p, st) : pick_norm<float, false>(p, st);
+}
+
+cudaError_t launch_quantize_rows(const ConvertParams &p, RowsType in, cudaStream_t st) {
+  int sms = 0;
+  const cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  const unsigned grid = convert_grid(p, sms);
+  if (in == RowsType::kBf16) {
+    if (aligned(p.x.data, p.x.ld, 2)) quantize_kernel<__nv_bfloat16, true><<<grid, 256, 0, st>>>(p);
+    else quantize_kernel<__nv_bfloat16, false><<<grid, 256, 0, st>>>(p);
+  } else {
+    if (aligned(p.x.data, p.x.ld, 4)) quantize_kernel<float, true><<<grid, 256, 0, st>>>(p);
+    else quantize_kernel<float, false><<<grid, 256, 0, st>>>(p);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_dequantize_rows(const ConvertParams &p, RowsType out, cudaStream_t st) {
+  int sms = 0;
+  const cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  const unsigned grid = convert_grid(p, sms);
+  if (out == RowsType::kBf16) {
+    if (aligned(p.out.data, p.out.ld, 2)) dequantize_kernel<__nv_bfloat16, true><<<grid, 256, 0, st>>>(p);
+    else dequantize_kernel<__nv_bfloat16, false><<<grid, 256, 0, st>>>(p);
+  } else {
+    if (aligned(p.out.data, p.out.ld, 4)) dequantize_kernel<float, true><<<grid, 256, 0, st>>>(p);
+    else dequantize_kernel<float, false><<<grid, 256, 0, st>>>(p);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace wf

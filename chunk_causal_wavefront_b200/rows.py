@@ -1,0 +1,262 @@
+"""Torch-facing row operators: residual addition + norm, linear, E4M3 rows.
+
+Rows are the last dimension's vectors: a tensor [..., cols] is taken as rows of
+cols elements. A round's activations [S+1][C][heads][d] are viewed as
+[(S+1) * C][heads * d]; the live slots are its first rows, so ``x[:n]`` of such a
+view (or one slot's rows) is what a fill round passes. Every computation runs in
+libwf's kernels; PyTorch allocates outputs that the caller does not give.
+
+The calls enqueue on ``stream`` (default: the tensors' device's current stream)
+and do not synchronise. They compute no gradients and refuse tensors that want
+them while gradients are recorded.
+"""
+from __future__ import annotations
+
+import contextlib
+from typing import Optional, Tuple, Union
+
+import torch
+
+from . import wf as _wf
+from .wf import WfError, WfRows
+
+_TYPES = {torch.bfloat16: _wf.WF_DTYPE_BF16, torch.float32: _wf.WF_DTYPE_F32}
+_ACTS = {"none": _wf.WF_ACT_NONE, "gelu": _wf.WF_ACT_GELU, "silu": _wf.WF_ACT_SILU}
+
+
+class E4M3Rows:
+    """Rows held as E4M3 codes with a power-of-two scale per 32 columns.
+
+    codes  : float8_e4m3fn [rows, cols], cols a multiple of 32, unit column stride
+    scales : uint8, wf_scale_bytes(rows, cols) bytes: e + 127 of each block (a
+             block's values are code * 2^e), in tiles of 128 rows x 4 blocks
+             (include/wf.h gives the order)
+    """
+
+    __slots__ = ("codes", "scales")
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor):
+        if codes.dim() != 2 or codes.dtype != torch.float8_e4m3fn:
+            raise ValueError("codes must be a float8_e4m3fn tensor [rows, cols]")
+        if scales.dtype != torch.uint8 or not scales.is_contiguous():
+            raise ValueError("scales must be a contiguous uint8 tensor")
+        rows, cols = codes.shape
+        if cols % 32 or cols == 0:
+            raise ValueError("E4M3 rows need a multiple of 32 columns")
+        if scales.numel() < (rows + 127) // 128 * ((cols + 127) // 128) * 512:
+            raise ValueError("scales has fewer than wf_scale_bytes(rows, cols) bytes")
+        if scales.device != codes.device:
+            raise ValueError("codes and scales must be on one device")
+        self.codes, self.scales = codes, scales
+
+    @classmethod
+    def empty(cls, rows: int, cols: int, device) -> "E4M3Rows":
+        n = _wf.wf_scale_bytes(rows, cols)
+        return cls(torch.empty(rows, cols, dtype=torch.float8_e4m3fn, device=device),
+                   torch.empty(n, dtype=torch.uint8, device=device))
+
+    @property
+    def shape(self) -> torch.Size:
+        return self.codes.shape
+
+    @property
+    def device(self) -> torch.device:
+        return self.codes.device
+
+    def first(self, rows: int) -> "E4M3Rows":
+        """The first rows, sharing memory."""
+        return E4M3Rows(self.codes[:rows], self.scales)
+
+    def dequantize(self, out: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.bfloat16,
+                   stream=None) -> torch.Tensor:
+        """The values these rows stand for, as bf16 or fp32 (exact in both)."""
+        with _on(stream, (self,), (out,)) as raw:
+            if out is None:
+                out = torch.empty(self.codes.shape, dtype=dtype, device=self.codes.device)
+            _check(_wf.wf_dequantize_rows(_rows(self), _rows(out), raw), "wf_dequantize_rows")
+        return out
+
+
+Operand = Union[torch.Tensor, E4M3Rows]
+
+
+def _rows(t: Optional[Operand]) -> Optional[WfRows]:
+    """The C description of rows; a view, never a copy."""
+    if t is None:
+        return None
+    if isinstance(t, E4M3Rows):
+        c = t.codes
+        if c.stride(1) != 1:
+            raise ValueError("rows must have unit column stride")
+        rows, cols = c.shape
+        ld = c.stride(0) if rows > 1 else max(c.stride(0), cols)
+        return WfRows(c.data_ptr() or None, t.scales.data_ptr() or None, rows, cols, ld,
+                      _wf.WF_DTYPE_FP8_E4M3)
+    code = _TYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"rows must be bfloat16, float32 or E4M3Rows, not {t.dtype}")
+    if t.dim() == 0 or t.shape[-1] == 0:
+        raise ValueError("rows must have at least one column")
+    cols = t.shape[-1]
+    if t.is_contiguous():
+        rows, ld = t.numel() // cols, cols
+    elif t.dim() == 2 and (t.stride(1) == 1 or cols == 1):
+        rows, ld = t.shape[0], t.stride(0)
+        if rows > 1 and ld < cols:
+            raise ValueError("rows that share memory (an expanded tensor) are not supported")
+        ld = max(ld, cols)
+    else:
+        raise ValueError("rows must be contiguous, or 2-D with unit column stride")
+    return WfRows(t.data_ptr() or None, None, rows, cols, ld, code)
+
+
+def _check(status: int, what: str) -> None:
+    if status != _wf.WF_OK:
+        raise WfError(status, what)
+
+
+@contextlib.contextmanager
+def _scope(device, stream):
+    with torch.cuda.device(device):
+        if stream is None:
+            yield torch.cuda.current_stream(device).cuda_stream
+        else:
+            with torch.cuda.stream(stream):   # outputs allocated here belong to the stream
+                yield stream.cuda_stream
+
+
+class _Here:
+    """The common case of _on: the tensors' device is current, no stream given."""
+
+    __slots__ = ("raw",)
+
+    def __init__(self, raw):
+        self.raw = raw
+
+    def __enter__(self):
+        return self.raw
+
+    def __exit__(self, *exc):
+        return False
+
+
+def _on(stream, inputs, outputs):
+    """Checks that everything is on one CUDA device and makes it current; gives the raw stream."""
+    device = None
+    grad = torch.is_grad_enabled()
+    for t in inputs + outputs:
+        if t is None:
+            continue
+        d = t.device
+        if device is None:
+            device = d
+            if d.type != "cuda":
+                raise ValueError("row operators need CUDA tensors")
+        elif d != device:
+            raise ValueError(f"all tensors must be on one device: got {device} and {d}")
+        if grad and not isinstance(t, E4M3Rows) and t.requires_grad:
+            raise ValueError("row operators compute no gradients: call them under torch.no_grad()")
+    if stream is None and device.index == torch.cuda.current_device():
+        return _Here(torch.cuda.current_stream(device).cuda_stream)
+    if stream is not None and stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    return _scope(device, stream)
+
+
+def _vector(v: Optional[torch.Tensor], n: int, name: str) -> Optional[int]:
+    if v is None:
+        return None
+    if v.dtype != torch.float32 or v.shape != (n,) or not v.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 vector of {n} elements")
+    return v.data_ptr()
+
+
+def _result(out: Optional[Operand], shape, out_dtype, default: torch.dtype, device) -> Operand:
+    """The caller's output after a check of its shape, or a new one."""
+    if out is not None:
+        if out_dtype is not None:
+            raise ValueError("give out or out_dtype, not both")
+        want = tuple(shape)
+        if isinstance(out, E4M3Rows):
+            n = 1
+            for s in want[:-1]:
+                n *= s
+            want = (n, want[-1])
+        if tuple(out.shape) != want:
+            raise ValueError(f"out has shape {tuple(out.shape)}, not {want}")
+        return out
+    if out_dtype == "e4m3":
+        rows = 1
+        for s in shape[:-1]:
+            rows *= s
+        return E4M3Rows.empty(rows, shape[-1], device)
+    if out_dtype is not None and out_dtype is not default:
+        raise ValueError(f"out_dtype must be {default} (the default) or 'e4m3'")
+    return torch.empty(shape, dtype=default, device=device)
+
+
+def quantize_rows(x: torch.Tensor, out: Optional[E4M3Rows] = None, stream=None) -> E4M3Rows:
+    """x [..., cols] in bf16 or fp32 as E4M3 rows (leading dimensions flattened)."""
+    with _on(stream, (x,), (out,)) as raw:
+        out = _result(out, x.shape, "e4m3" if out is None else None, x.dtype, x.device)
+        _check(_wf.wf_quantize_rows(_rows(x), _rows(out), raw), "wf_quantize_rows")
+    return out
+
+
+def add_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *,
+                 residual: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                 out: Optional[Operand] = None, sum_out: Optional[torch.Tensor] = None,
+                 out_dtype=None, stream=None) -> Union[Operand, Tuple[Operand, torch.Tensor]]:
+    """s = x + residual; out = s / sqrt(mean(s^2) + eps) * weight, row by row.
+
+    Without a residual returns out, with one (out, s). out has x's type, or is
+    E4M3Rows with out_dtype="e4m3" (or out=E4M3Rows). sum_out may be x or
+    residual: the residual stream is then updated in place. weight is float32.
+    """
+    if residual is None and sum_out is not None:
+        raise ValueError("sum_out needs a residual")
+    if residual is not None and residual.shape != x.shape:
+        raise ValueError(f"residual has shape {tuple(residual.shape)}, x {tuple(x.shape)}")
+    if sum_out is not None and sum_out.shape != x.shape:
+        raise ValueError(f"sum_out has shape {tuple(sum_out.shape)}, x {tuple(x.shape)}")
+    with _on(stream, (x, weight, residual), (out, sum_out)) as raw:
+        w = _vector(weight, x.shape[-1], "weight")
+        out = _result(out, x.shape, out_dtype, x.dtype, x.device)
+        if residual is not None and sum_out is None:
+            sum_out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        _check(_wf.wf_add_rms_norm(_rows(x), _rows(residual), w, eps, _rows(sum_out),
+                                   _rows(out), raw), "wf_add_rms_norm")
+    return out if residual is None else (out, sum_out)
+
+
+def linear(x: Operand, w: Operand, bias: Optional[torch.Tensor] = None, *, act: str = "none",
+           residual: Optional[torch.Tensor] = None, out: Optional[Operand] = None,
+           out_dtype=None, stream=None) -> Operand:
+    """act(x w^T + bias) + residual on the tensor cores, accumulated in fp32.
+
+    x [..., K] and w [N, K] are both bf16 or both E4M3Rows; bias is float32 [N];
+    act is "none", "gelu" (tanh form) or "silu". The result is bf16 [..., N], or
+    E4M3Rows with out_dtype="e4m3" (or out=E4M3Rows), then without a residual.
+    out may be residual itself.
+    """
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}")
+    if len(w.shape) != 2 or len(x.shape) == 0 or x.shape[-1] != w.shape[1]:
+        raise ValueError(f"shapes {tuple(x.shape)} and {tuple(w.shape)} do not give x w^T")
+    shape = tuple(x.shape[:-1]) + (w.shape[0],)
+    if residual is not None and tuple(residual.shape) != shape:
+        raise ValueError(f"residual has shape {tuple(residual.shape)}, not {shape}")
+    with _on(stream, (x, w, bias, residual), (out,)) as raw:
+        b = _vector(bias, w.shape[0], "bias")
+        out = _result(out, shape, out_dtype, torch.bfloat16, x.device)
+        _check(_wf.wf_linear(_rows(x), _rows(w), b, _ACTS[act], _rows(residual), _rows(out),
+                             raw), "wf_linear")
+    return out
+
+
+def rows_check_status(device=None, stream=None) -> int:
+    """Synchronise, then return and clear the device's row-operator status."""
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    with torch.cuda.device(device):
+        s = torch.cuda.current_stream(device) if stream is None else stream
+        return _wf.wf_rows_check_status(s.cuda_stream)

@@ -29,6 +29,9 @@ WF_ROPE_OFF = 0
 WF_ROPE_3D = 1
 WF_MASK_WF = 0
 WF_MASK_RF = 1
+WF_ACT_NONE = 0
+WF_ACT_GELU = 1
+WF_ACT_SILU = 2
 KIND_NAMES = {0: "anchor", 1: "history", 2: "store", 3: "slot"}
 
 EXPORTS = (
@@ -37,7 +40,8 @@ EXPORTS = (
     "wf_pool_round", "wf_pool_get_geometry", "wf_pool_get_layout", "wf_pool_debug_poke_page",
     "wf_project_publish", "wf_publish_kv_slot", "wf_round_attention_slot", "wf_deliver_kv",
     "wf_pool_debug_stall_next_attention", "wf_ipc_get_mem_handle", "wf_ipc_open_mem",
-    "wf_ipc_close_mem",
+    "wf_ipc_close_mem", "wf_scale_bytes", "wf_quantize_rows", "wf_dequantize_rows",
+    "wf_add_rms_norm", "wf_linear", "wf_rows_check_status",
 )
 
 
@@ -69,6 +73,13 @@ class WfIpcHandle(ctypes.Structure):
     _fields_ = [("bytes", ctypes.c_ubyte * 64)]
 
 
+class WfRows(ctypes.Structure):
+    _fields_ = [
+        ("data", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64), ("ld", ctypes.c_int64), ("dtype", ctypes.c_int32),
+    ]
+
+
 class WfError(RuntimeError):
     def __init__(self, status: int, what: str = ""):
         self.status = int(status)
@@ -85,6 +96,7 @@ def _load():
     P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     cfgp = ctypes.POINTER(WfPoolConfig)
     i32p = ctypes.POINTER(ctypes.c_int32)
+    rowsp, F32 = ctypes.POINTER(WfRows), ctypes.c_float
     sig = {
         "wf_kv_pool_bytes": (I32, [cfgp, ctypes.POINTER(SZ)]),
         "wf_kv_pool_create": (I32, [cfgp, P, SZ, i32p, P, ctypes.POINTER(P)]),
@@ -106,6 +118,12 @@ def _load():
         "wf_ipc_get_mem_handle": (I32, [P, ctypes.POINTER(WfIpcHandle), ctypes.POINTER(SZ)]),
         "wf_ipc_open_mem": (I32, [ctypes.POINTER(WfIpcHandle), SZ, ctypes.POINTER(P)]),
         "wf_ipc_close_mem": (I32, [P, SZ]),
+        "wf_scale_bytes": (I32, [I64, I64, ctypes.POINTER(SZ)]),
+        "wf_quantize_rows": (I32, [rowsp, rowsp, P]),
+        "wf_dequantize_rows": (I32, [rowsp, rowsp, P]),
+        "wf_add_rms_norm": (I32, [rowsp, rowsp, P, F32, rowsp, rowsp, P]),
+        "wf_linear": (I32, [rowsp, rowsp, P, I32, rowsp, rowsp, P]),
+        "wf_rows_check_status": (I32, [P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -255,3 +273,33 @@ def wf_pool_debug_poke_page(pool: int, position: int, j: int, physical: int, str
 
 def wf_project_publish(pool: int, layer: int, x: int, w_qkv: int, q_rot: int, stream: int) -> int:
     return _lib.wf_project_publish(pool, layer, x, w_qkv, q_rot, ctypes.c_void_p(stream or None))
+
+
+def wf_scale_bytes(rows: int, cols: int) -> int:
+    n = ctypes.c_size_t(0)
+    st = _lib.wf_scale_bytes(rows, cols, ctypes.byref(n))
+    if st != WF_OK:
+        raise WfError(st, "wf_scale_bytes")
+    return n.value
+
+
+def wf_quantize_rows(x: WfRows, out: WfRows, stream: int) -> int:
+    return _lib.wf_quantize_rows(x, out, stream or None)
+
+
+def wf_dequantize_rows(x: WfRows, out: WfRows, stream: int) -> int:
+    return _lib.wf_dequantize_rows(x, out, stream or None)
+
+
+def wf_add_rms_norm(x: WfRows, residual: Optional[WfRows], weight: Optional[int], eps: float,
+                    sum_out: Optional[WfRows], out: WfRows, stream: int) -> int:
+    return _lib.wf_add_rms_norm(x, residual, weight, eps, sum_out, out, stream or None)
+
+
+def wf_linear(x: WfRows, w: WfRows, bias: Optional[int], act: int, residual: Optional[WfRows],
+              out: WfRows, stream: int) -> int:
+    return _lib.wf_linear(x, w, bias, act, residual, out, stream or None)
+
+
+def wf_rows_check_status(stream: int) -> int:
+    return _lib.wf_rows_check_status(stream or None)

@@ -1,6 +1,7 @@
 /*
  * wf.h - C ABI of libwf: one causal-wavefront round of chunk-wise causal
- * attention (Wave Forcing), on one NVIDIA B200 (sm_100a).
+ * attention (Wave Forcing), and the row operators of a layer around it, on one
+ * NVIDIA B200 (sm_100a).
  *
  * Source: "Wave Forcing: Towards Speed-of-Light Streaming Video Generation"
  * (arXiv 2611.00859). The method, as the pages state it:
@@ -341,6 +342,89 @@ wf_status wf_pool_debug_poke_page(wf_pool *pool, int32_t position, int32_t j,
  * unaffected. bf16 and FP8_E4M3 pools only (WF_ERR_UNSUPPORTED for fp32). */
 wf_status wf_pool_debug_stall_next_attention(wf_pool *pool, int32_t key_tile,
                                              int64_t wait_limit_cycles);
+
+/* ------------------------------------------------------------ row operators --
+ * What a transformer layer runs around its round attention, over rows (tokens)
+ * of features: the residual addition with its norm, matrix products with
+ * their epilogue, and the 8-bit form of both (the W8A8 products that Tables 4-6
+ * of the appendix pair with the 8-bit attention backends). They need no pool. A
+ * round's activations [S+1][C][heads][d] are (S+1) * C rows of heads * d
+ * columns; the live slots are a prefix of them (one slot: its own C rows).
+ *
+ * E4M3 rows: codes, one byte per element, and one scale byte per row and block
+ * of 32 columns: the block stands for code * 2^e, the byte is e + 127, and e is
+ * the smallest integer >= -100 with amax * 2^-e <= 448 (amax over the block's
+ * values that are not NaN; e <= 120). Codes are rounded to nearest even; NaN
+ * stays NaN, and infinities become +-448 * 2^120, which is infinite again in
+ * bf16 and fp32. The scale bytes lie in tiles of 128 rows x 4 blocks, as the
+ * block-scaled tensor-core products read them: the byte of row r, block b is at
+ *     ((r / 128) * ceil(blocks / 4) + b / 4) * 512
+ *         + (r % 32) * 16 + (r / 32 % 4) * 4 + b % 4,
+ * so the first n rows of E4M3 rows are E4M3 rows too. Bytes of rows or blocks
+ * past the end are neither written nor used.
+ *
+ * Every wf_rows struct is a HOST pointer; its data and scales, the weight and
+ * the bias are device pointers on the current device. Rows may be strided
+ * (ld >= cols; the ld of a single row is not used). Outputs must not overlap
+ * each other or an input, except where a call says that it may run in place.
+ * rows = 0 is allowed and does nothing. */
+typedef struct {
+  void *data;      /* elements [rows][ld] of dtype (E4M3: codes) */
+  void *scales;    /* E4M3: wf_scale_bytes(rows, cols) bytes, 16-byte aligned; else ignored */
+  int64_t rows;    /* 0 .. 2^31 - 256 */
+  int64_t cols;    /* 1 .. 2^31 - 256; E4M3: a multiple of 32 */
+  int64_t ld;      /* elements from one row to the next; E4M3: a multiple of 16 */
+  int32_t dtype;   /* WF_DTYPE_BF16, WF_DTYPE_F32 or WF_DTYPE_FP8_E4M3 */
+} wf_rows;
+
+/* Activation of wf_linear. GELU is the tanh form
+ * v / (1 + exp(-2 sqrt(2 / pi) (v + 0.044715 v^3))); SILU is v / (1 + exp(-v)). */
+enum { WF_ACT_NONE = 0, WF_ACT_GELU = 1, WF_ACT_SILU = 2 };
+
+/* Bytes of the scales of E4M3 rows: ceil(rows / 128) * ceil(cols / 128) * 512.
+ * WF_ERR_INVALID_ARG unless cols is a positive multiple of 32. */
+wf_status wf_scale_bytes(int64_t rows, int64_t cols, size_t *bytes);
+
+/* out = x as E4M3 rows. x is bf16 or fp32, out E4M3 of the same shape. */
+wf_status wf_quantize_rows(const wf_rows *x, const wf_rows *out, wf_stream_t stream);
+
+/* out = the values that E4M3 rows stand for, as bf16 or fp32. Both are exact,
+ * but for values past the type's range, which become infinite. */
+wf_status wf_dequantize_rows(const wf_rows *x, const wf_rows *out, wf_stream_t stream);
+
+/* Residual addition and root-mean-square norm of every row:
+ *     s = x + residual,   sum = s,   out = s / sqrt(mean(s^2) + eps) * weight
+ * in fp32, each output rounded once (out from the unrounded s).
+ *   x, residual : bf16 or fp32, the same type and shape; residual may be NULL.
+ *   weight      : fp32 [cols], or NULL for ones.
+ *   eps         : finite, >= 0.
+ *   sum         : type and shape of x, or NULL; may be x or residual itself
+ *                 (same data and ld).
+ *   out         : type and shape of x, or E4M3 rows; in x's type it may be x or
+ *                 residual itself (then sum must be another buffer or NULL). */
+wf_status wf_add_rms_norm(const wf_rows *x, const wf_rows *residual, const float *weight,
+                          float eps, const wf_rows *sum, const wf_rows *out, wf_stream_t stream);
+
+/* Matrix product with its epilogue:
+ *     out = act(x w^T + bias) + residual
+ * accumulated in fp32 on the tensor cores, the epilogue in fp32, rounded once.
+ *   x        : [M][K], w : [N][K] (row n: weights of output feature n), both
+ *              bf16 or both E4M3 rows; data 16-byte aligned and ld * element
+ *              size a multiple of 16 (WF_ERR_INVALID_ARG otherwise).
+ *   bias     : fp32 [N], or NULL.
+ *   act      : WF_ACT_*.
+ *   residual : bf16 [M][N], or NULL; only with a bf16 out, which may be residual
+ *              itself (same data and ld).
+ *   out      : [M][N], bf16 or E4M3 rows.
+ * WF_ERR_UNSUPPORTED for fp32 operands or output, for operands of two types and
+ * for a residual with an E4M3 output. A device-side wait that runs out is
+ * recorded in the device's row-operator status; out is then undefined. */
+wf_status wf_linear(const wf_rows *x, const wf_rows *w, const float *bias, int32_t act,
+                    const wf_rows *residual, const wf_rows *out, wf_stream_t stream);
+
+/* Synchronise the stream, then return and clear the current device's sticky
+ * row-operator status (WF_OK, or WF_ERR_TIMEOUT from a wf_linear call). */
+wf_status wf_rows_check_status(wf_stream_t stream);
 
 #ifdef __cplusplus
 }
