@@ -15,13 +15,18 @@
 // Tiles are walked in groups of 8 row tiles, feature tiles slowest inside a
 // group, so that the tiles in flight cover a near-square patch of the output and
 // both operands are re-read from L2.
-//   warp 8 (one lane)  TMA producer of its CTA (128-byte swizzled operand boxes,
+//   warp 8             TMA producer of its CTA (128-byte swizzled operand boxes,
 //                      for E4M3 also the 512-byte scale tiles: one of x, and two
 //                      that cover the BN features of w in both CTAs); all bytes
 //                      count on the leader's full barrier.
-//   warp 9 (one lane)  leader only: copies the stage's scales into TMEM, then
+//   warp 9             leader only: copies the stage's scales into TMEM, then
 //                      issues the MMAs; k-steps past K are not issued, so scale
 //                      bytes past the last block are never used.
+//   Both run as whole warps that elect a lane for each stage: with a branch on the
+//   lane number around the loop, the operands of every tcgen05 instruction go
+//   through registers, about 140 cycles apiece, and the issue bounds the kernel
+//   (4680 x 20480 x 5120 bf16 716 us against 668, 23400 x 1536 x 6144 E4M3 228
+//   against 187).
 //   warps 0-7          epilogue: warpgroup e takes columns [e BN/2, (e+1) BN/2)
 //                      of the CTA's 128 rows, a thread owns one row and 32
 //                      columns at a time. The residual's 32 x 32 box comes in by
@@ -110,11 +115,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::kOffBar);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::kOffMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + S::kOffMisc + 4);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int pair = static_cast<int>(blockIdx.x >> 1), npairs = static_cast<int>(gridDim.x >> 1);
 
   if (threadIdx.x == 0) {
+    tma_prefetch_desc(&tx);
+    tma_prefetch_desc(&tw);
     *abort_flag = 0;
     for (int b = 0; b < S::kNumBars; ++b)
       mbar_init(bars + b, (b == S::kAccEmpty0 || b == S::kAccEmpty0 + 1) ? 2 * kEpiWarps : 1);
@@ -132,26 +139,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (warp == kProducerWarp) {
     // ------------------------------------------------------------ producer --
-    if (lane == 0) {
-      tma_prefetch_desc(&tx);
-      tma_prefetch_desc(&tw);
-      if constexpr (MX) {
-        tma_prefetch_desc(&tsx);
-        tma_prefetch_desc(&tsw);
-      }
-      int q = 0;                            // k-blocks issued by this CTA
-      bool ok = true;
-      for (int t = pair; ok && t < g.total; t += npairs) {
-        int mt, nt;
-        decode(g, t, mt, nt);
-        const int row0 = mt * 256 + static_cast<int>(rank) * 128;
-        const int col0 = nt * BN;
-        for (int kb = 0; kb < g.n_kb; ++kb, ++q) {
-          const int s = q % S::kStages;
-          if (!wait_bar(ctx, S::kEmpty0 + s, ((q / S::kStages) & 1) ^ 1)) {
-            ok = false;
-            break;
-          }
+    int q = 0;                              // k-blocks issued by this CTA
+    bool ok = true;
+    for (int t = pair; ok && t < g.total; t += npairs) {
+      int mt, nt;
+      decode(g, t, mt, nt);
+      const int row0 = mt * 256 + static_cast<int>(rank) * 128;
+      const int col0 = nt * BN;
+      for (int kb = 0; kb < g.n_kb; ++kb, ++q) {
+        const int s = q % S::kStages;
+        ok = __all_sync(0xffffffffu, wait_bar(ctx, S::kEmpty0 + s, ((q / S::kStages) & 1) ^ 1));
+        if (!ok) break;
+        if (elect_one()) {
           // The leader expects the bytes of both CTAs on its full barrier.
           if (rank == 0) mbar_arrive_expect_tx(bars + S::kFull0 + s, 2 * S::kStageBytes);
           uint8_t *sa = smem + s * S::kOperandBytes;
@@ -164,17 +163,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tma_load_3d_pair(ss + 512, &tsw, lb, 0, kb, col0 >> 7);
           }
         }
+        __syncwarp();
       }
-      // Tail: every stage this CTA filled has been consumed by the MMAs, so no
-      // load of this CTA is in flight when it exits.
-      for (int s = 0; s < S::kStages && q > 0; ++s) {
-        const int fills = q / S::kStages + (s < q % S::kStages ? 1 : 0);
-        if (fills > 0) drain_wait(ctx, S::kEmpty0 + s, (fills - 1) & 1);
-      }
+    }
+    // Tail: every stage this CTA filled has been consumed by the MMAs, so no
+    // load of this CTA is in flight when it exits.
+    for (int s = 0; s < S::kStages && q > 0; ++s) {
+      const int fills = q / S::kStages + (s < q % S::kStages ? 1 : 0);
+      if (fills > 0) drain_wait(ctx, S::kEmpty0 + s, (fills - 1) & 1);
     }
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------- MMA issuer --
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       const uint32_t hi = desc_hi_sw128(1024);
       const uint32_t lo0 = desc_lo_sw128(smem_u32(smem), 16);
       const uint32_t sc0 = smem_u32(smem + S::kOffScale);
@@ -184,13 +184,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int mt, nt;
         decode(g, t, mt, nt);
         const int b = i & 1;
-        if (!wait_bar_cluster(ctx, S::kAccEmpty0 + b, ((i >> 1) & 1) ^ 1)) break;
+        if (!__all_sync(0xffffffffu, wait_bar_cluster(ctx, S::kAccEmpty0 + b, ((i >> 1) & 1) ^ 1))) break;
         tc_fence_after();
         // BN = 192: odd feature tiles start at row 64 of a 128-row scale tile.
         const uint32_t shift = (nt * BN & 127) >> 5;
         for (int kb = 0; kb < g.n_kb; ++kb, ++q) {
           const int s = q % S::kStages;
-          if (!wait_bar_cluster(ctx, S::kFull0 + s, (q / S::kStages) & 1)) {
+          if (!__all_sync(0xffffffffu, wait_bar_cluster(ctx, S::kFull0 + s, (q / S::kStages) & 1))) {
             ok = false;
             break;
           }
@@ -198,33 +198,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t a_lo = lo0 + ((s * S::kOperandBytes) >> 4);
           const uint32_t b_lo = a_lo + (kABytes >> 4);
           const int left = g.k_steps - kb * (S::kKElems / S::kKStep);
-          if constexpr (MX) {
-            const uint32_t sc = sc0 + s * S::kScaleBytes;
-            const uint32_t sfa = tmem + kScaleCols + 16 * (q & 3);
-            const uint32_t sfb = sfa + 4;
-            tmem_copy_scales_pair(sfa, make_desc_scale_tile(sc));
-            tmem_copy_scales_pair(sfb, make_desc_scale_tile(sc + 512));
-            tmem_copy_scales_pair(sfb + 4, make_desc_scale_tile(sc + 1024));
+          if (elect_one()) {
+            if constexpr (MX) {
+              const uint32_t sc = sc0 + s * S::kScaleBytes;
+              const uint32_t sfa = tmem + kScaleCols + 16 * (q & 3);
+              const uint32_t sfb = sfa + 4;
+              tmem_copy_scales_pair(sfa, make_desc_scale_tile(sc));
+              tmem_copy_scales_pair(sfb, make_desc_scale_tile(sc + 512));
+              tmem_copy_scales_pair(sfb + 4, make_desc_scale_tile(sc + 1024));
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (k < left)
-                mma_mx_ss2_pair(tmem + BN * b, a_lo + k * 2, b_lo + k * 2, hi,
-                                make_idesc_mx_e4m3(256, BN, k), sfa, sfb + shift,
-                                (kb > 0 || k > 0) ? 1u : 0u);
-          } else {
-            constexpr uint32_t idesc = make_idesc_bf16(256, BN, false);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (k < left)
-                mma_bf16_ss2_pair(tmem + BN * b, a_lo + k * 2, b_lo + k * 2, hi, idesc,
+              for (int k = 0; k < 4; ++k)
+                if (k < left)
+                  mma_mx_ss2_pair(tmem + BN * b, a_lo + k * 2, b_lo + k * 2, hi,
+                                  make_idesc_mx_e4m3(256, BN, k), sfa, sfb + shift,
                                   (kb > 0 || k > 0) ? 1u : 0u);
+            } else {
+              constexpr uint32_t idesc = make_idesc_bf16(256, BN, false);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (k < left)
+                  mma_bf16_ss2_pair(tmem + BN * b, a_lo + k * 2, b_lo + k * 2, hi, idesc,
+                                    (kb > 0 || k > 0) ? 1u : 0u);
+            }
+            mma_commit_pair(bars + S::kEmpty0 + s);
           }
-          mma_commit_pair(bars + S::kEmpty0 + s);
+          __syncwarp();
         }
-        if (ok) mma_commit_pair(bars + S::kAccFull0 + b);
+        if (ok && elect_one()) mma_commit_pair(bars + S::kAccFull0 + b);
+        __syncwarp();
       }
       // Drain: all MMAs issued by this thread complete before TMEM is freed.
-      mma_commit_pair(bars + S::kDrain);
+      if (elect_one()) mma_commit_pair(bars + S::kDrain);
+      __syncwarp();
       drain_wait(ctx, S::kDrain, 0);
     }
   } else {
@@ -409,10 +414,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 template <bool MX, int BN, bool OUT8>
 cudaError_t run_pair(const LinearParams &p, cudaStream_t st) {
   using S = Shape<MX, BN>;
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
   const int elt = MX ? 1 : 2;
   CUtensorMap tx{}, tw{}, tsx{}, tsw{}, tr{}, to{};
   const uint64_t K = static_cast<uint64_t>(p.K), M = static_cast<uint64_t>(p.M), N = static_cast<uint64_t>(p.N);
@@ -448,10 +449,10 @@ cudaError_t run_pair(const LinearParams &p, cudaStream_t st) {
   g.k_steps = (p.K + S::kKStep - 1) / S::kKStep;
   g.out_block_tiles = (p.N + 127) / 128;
   g.has_residual = p.residual.data != nullptr;
-  e = cudaFuncSetAttribute(linear_pair_kernel<MX, BN, OUT8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(S::kSmemBytes));
+  static std::atomic<uint64_t> allowed;
+  const cudaError_t e = allow_shared(linear_pair_kernel<MX, BN, OUT8>, allowed, p.device, S::kSmemBytes);
   if (e != cudaSuccess) return e;
-  const int pairs = g.total < sms / 2 ? g.total : sms / 2;
+  const int pairs = g.total < p.sms / 2 ? g.total : p.sms / 2;
   linear_pair_kernel<MX, BN, OUT8><<<2 * pairs, kThreads, S::kSmemBytes, st>>>(p, g, tx, tw, tsx, tsw, tr, to);
   return cudaGetLastError();
 }

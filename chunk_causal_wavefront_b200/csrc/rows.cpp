@@ -220,13 +220,14 @@ wf_status wf_linear(const wf_rows *x, const wf_rows *w, const float *bias, int32
   p.M = static_cast<int32_t>(x->rows);
   p.N = static_cast<int32_t>(w->rows);
   p.K = static_cast<int32_t>(x->cols);
-  if (rows_status_word(&p.status) != cudaSuccess) return WF_ERR_CUDA;
+  DeviceFacts dev;
+  if (device_facts(&dev) != cudaSuccess) return WF_ERR_CUDA;
+  p.status = dev.status;
+  p.device = dev.device;
+  p.sms = dev.sms;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool stored_by_tma = rows16(out) && (!residual || rows16(residual));
-  int sms = 0, dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return WF_ERR_CUDA;
+  const int sms = dev.sms;
   const int64_t m_tiles = (x->rows + 255) / 256;
   if (stored_by_tma && x->rows > 128 && m_tiles * ((w->rows + 191) / 192) >= sms / 4) {
     // Waves of CTA pairs times the tile's width: what the last wave wastes.
@@ -245,11 +246,11 @@ wf_status wf_linear(const wf_rows *x, const wf_rows *w, const float *bias, int32
 
 wf_status wf_rows_check_status(wf_stream_t stream) {
   if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return WF_ERR_CUDA;
-  int32_t *word = nullptr;
-  if (rows_status_word(&word) != cudaSuccess) return WF_ERR_CUDA;
+  DeviceFacts dev;
+  if (device_facts(&dev) != cudaSuccess) return WF_ERR_CUDA;
   int32_t v = 0;
-  if (cudaMemcpy(&v, word, 4, cudaMemcpyDeviceToHost) != cudaSuccess) return WF_ERR_CUDA;
-  if (v != 0 && cudaMemset(word, 0, 4) != cudaSuccess) return WF_ERR_CUDA;
+  if (cudaMemcpy(&v, dev.status, 4, cudaMemcpyDeviceToHost) != cudaSuccess) return WF_ERR_CUDA;
+  if (v != 0 && cudaMemset(dev.status, 0, 4) != cudaSuccess) return WF_ERR_CUDA;
   return static_cast<wf_status>(v);
 }
 

@@ -20,6 +20,8 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <new>
+
 #include "rows.cuh"
 #include "sm100.cuh"
 
@@ -307,28 +309,27 @@ bool aligned(const void *p, int64_t ld, int64_t elt) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (ld * elt) % 16 == 0;
 }
 
-cudaError_t sm_count(int *sms) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
-  return e;
-}
-
 // Blocks that the device holds at once: a grid of that size walks the rows with
-// the weight in registers and no second wave.
+// the weight in registers and no second wave. Asked once per kernel and device.
 template <typename K>
-cudaError_t resident_blocks(K kernel, int threads, int sms, int64_t *blocks) {
-  int per_sm = 0;
-  const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, 0);
-  *blocks = static_cast<int64_t>(per_sm > 0 ? per_sm : 1) * sms;
-  return e;
+cudaError_t resident_blocks(K kernel, std::atomic<int> (&known)[64], const DeviceFacts &dev, int64_t *blocks) {
+  int per_sm = dev.device < 64 ? known[dev.device].load(std::memory_order_relaxed) : 0;
+  if (per_sm == 0) {
+    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kNormThreads, 0);
+    if (e != cudaSuccess) return e;
+    if (per_sm < 1) per_sm = 1;
+    if (dev.device < 64) known[dev.device].store(per_sm, std::memory_order_relaxed);
+  }
+  *blocks = static_cast<int64_t>(per_sm) * dev.sms;
+  return cudaSuccess;
 }
 
 template <typename T, bool OUT8, int WPR, int CH>
-cudaError_t run_norm(const NormParams &p, int sms, cudaStream_t st) {
+cudaError_t run_norm(const NormParams &p, const DeviceFacts &dev, cudaStream_t st) {
   constexpr int kRows = kNormThreads / 32 / WPR;
+  static std::atomic<int> known[64];
   int64_t grid = 0;
-  const cudaError_t e = resident_blocks(norm_kernel<T, OUT8, WPR, CH>, kNormThreads, sms, &grid);
+  const cudaError_t e = resident_blocks(norm_kernel<T, OUT8, WPR, CH>, known, dev, &grid);
   if (e != cudaSuccess) return e;
   const int64_t need = (p.rows + kRows - 1) / kRows;
   norm_kernel<T, OUT8, WPR, CH><<<static_cast<unsigned>(need < grid ? need : grid), kNormThreads, 0, st>>>(p);
@@ -337,8 +338,8 @@ cudaError_t run_norm(const NormParams &p, int sms, cudaStream_t st) {
 
 template <typename T, bool OUT8>
 cudaError_t pick_norm(const NormParams &p, cudaStream_t st) {
-  int sms = 0;
-  const cudaError_t e = sm_count(&sms);
+  DeviceFacts dev;
+  const cudaError_t e = device_facts(&dev);
   if (e != cudaSuccess) return e;
   const int64_t elt = sizeof(T);
   const bool vec = p.cols % 8 == 0 && p.cols <= 8192 && aligned(p.x.data, p.x.ld, elt) &&
@@ -347,23 +348,23 @@ cudaError_t pick_norm(const NormParams &p, cudaStream_t st) {
                    aligned(p.out.data, p.out.ld, OUT8 ? 1 : elt) &&
                    (reinterpret_cast<uintptr_t>(p.weight) & 15u) == 0;
   if (!vec) {
-    const int64_t grid = static_cast<int64_t>(sms) * 8;
+    const int64_t grid = static_cast<int64_t>(dev.sms) * 8;
     norm_any_kernel<T, OUT8><<<static_cast<unsigned>(p.rows < grid ? p.rows : grid), kNormThreads, 0, st>>>(p);
     return cudaGetLastError();
   }
   // Fewest warps per row that keep it at three chunks a lane (24 fp32 values,
   // as many weights, and the raw loads in flight).
   const int per_warp = (p.cols + 255) / 256;         // chunks per lane with one warp
-  if (per_warp <= 1) return run_norm<T, OUT8, 1, 1>(p, sms, st);
-  if (per_warp <= 2) return run_norm<T, OUT8, 1, 2>(p, sms, st);
-  if (per_warp <= 3) return run_norm<T, OUT8, 1, 3>(p, sms, st);
-  if (per_warp <= 4) return run_norm<T, OUT8, 2, 2>(p, sms, st);
-  if (per_warp <= 6) return run_norm<T, OUT8, 2, 3>(p, sms, st);
-  if (per_warp <= 8) return run_norm<T, OUT8, 4, 2>(p, sms, st);
-  if (per_warp <= 12) return run_norm<T, OUT8, 4, 3>(p, sms, st);
-  if (per_warp <= 16) return run_norm<T, OUT8, 8, 2>(p, sms, st);
-  if (per_warp <= 24) return run_norm<T, OUT8, 8, 3>(p, sms, st);
-  return run_norm<T, OUT8, 8, 4>(p, sms, st);
+  if (per_warp <= 1) return run_norm<T, OUT8, 1, 1>(p, dev, st);
+  if (per_warp <= 2) return run_norm<T, OUT8, 1, 2>(p, dev, st);
+  if (per_warp <= 3) return run_norm<T, OUT8, 1, 3>(p, dev, st);
+  if (per_warp <= 4) return run_norm<T, OUT8, 2, 2>(p, dev, st);
+  if (per_warp <= 6) return run_norm<T, OUT8, 2, 3>(p, dev, st);
+  if (per_warp <= 8) return run_norm<T, OUT8, 4, 2>(p, dev, st);
+  if (per_warp <= 12) return run_norm<T, OUT8, 4, 3>(p, dev, st);
+  if (per_warp <= 16) return run_norm<T, OUT8, 8, 2>(p, dev, st);
+  if (per_warp <= 24) return run_norm<T, OUT8, 8, 3>(p, dev, st);
+  return run_norm<T, OUT8, 8, 4>(p, dev, st);
 }
 
 unsigned convert_grid(const ConvertParams &p, int sms) {
@@ -377,11 +378,28 @@ unsigned convert_grid(const ConvertParams &p, int sms) {
 // Sticky status of the row operators that wait on barriers: one word per device.
 __device__ int32_t g_rows_status;
 
-cudaError_t rows_status_word(int32_t **word) {
-  void *p = nullptr;
-  const cudaError_t e = cudaGetSymbolAddress(&p, g_rows_status);
-  *word = static_cast<int32_t *>(p);
-  return e;
+cudaError_t device_facts(DeviceFacts *facts) {
+  static std::atomic<const DeviceFacts *> known[64];   // entries live as long as the process
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64) {
+    if (const DeviceFacts *f = known[dev].load(std::memory_order_acquire)) {
+      *facts = *f;
+      return cudaSuccess;
+    }
+  }
+  void *word = nullptr;
+  facts->device = dev;
+  e = cudaDeviceGetAttribute(&facts->sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) e = cudaGetSymbolAddress(&word, g_rows_status);
+  if (e != cudaSuccess) return e;
+  facts->status = static_cast<int32_t *>(word);
+  if (dev < 64) {
+    const DeviceFacts *fresh = new (std::nothrow) DeviceFacts(*facts), *none = nullptr;
+    if (fresh && !known[dev].compare_exchange_strong(none, fresh, std::memory_order_release)) delete fresh;
+  }
+  return cudaSuccess;
 }
 
 cudaError_t launch_add_rms_norm(const NormParams &p, RowsType in, bool out_e4m3, cudaStream_t st) {
@@ -391,10 +409,10 @@ cudaError_t launch_add_rms_norm(const NormParams &p, RowsType in, bool out_e4m3,
 }
 
 cudaError_t launch_quantize_rows(const ConvertParams &p, RowsType in, cudaStream_t st) {
-  int sms = 0;
-  const cudaError_t e = sm_count(&sms);
+  DeviceFacts dev;
+  const cudaError_t e = device_facts(&dev);
   if (e != cudaSuccess) return e;
-  const unsigned grid = convert_grid(p, sms);
+  const unsigned grid = convert_grid(p, dev.sms);
   if (in == RowsType::kBf16) {
     if (aligned(p.x.data, p.x.ld, 2)) quantize_kernel<__nv_bfloat16, true><<<grid, 256, 0, st>>>(p);
     else quantize_kernel<__nv_bfloat16, false><<<grid, 256, 0, st>>>(p);
@@ -406,10 +424,10 @@ cudaError_t launch_quantize_rows(const ConvertParams &p, RowsType in, cudaStream
 }
 
 cudaError_t launch_dequantize_rows(const ConvertParams &p, RowsType out, cudaStream_t st) {
-  int sms = 0;
-  const cudaError_t e = sm_count(&sms);
+  DeviceFacts dev;
+  const cudaError_t e = device_facts(&dev);
   if (e != cudaSuccess) return e;
-  const unsigned grid = convert_grid(p, sms);
+  const unsigned grid = convert_grid(p, dev.sms);
   if (out == RowsType::kBf16) {
     if (aligned(p.out.data, p.out.ld, 2)) dequantize_kernel<__nv_bfloat16, true><<<grid, 256, 0, st>>>(p);
     else dequantize_kernel<__nv_bfloat16, false><<<grid, 256, 0, st>>>(p);

@@ -7,6 +7,7 @@
 // products, so the scales never touch the CUDA cores again.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -39,6 +40,7 @@ struct LinearParams {
   int32_t act;
   int32_t M, N, K;
   int32_t *status;                  // the device's row-operator status word
+  int32_t device, sms;
 };
 
 enum class RowsType { kBf16, kF32, kE4m3 };
@@ -53,8 +55,23 @@ cudaError_t launch_linear_pair(const LinearParams &p, bool e4m3, bool out_e4m3, 
 // over a cluster of `split` CTAs, `nt` tokens per tile.
 cudaError_t launch_linear_skinny(const LinearParams &p, bool e4m3, bool out_e4m3, int nt,
                                  int split, cudaStream_t st);
-// The current device's row-operator status word.
-cudaError_t rows_status_word(int32_t **word);
+// What a launch needs to know of the current device; asked of the runtime once per
+// device, since the queries cost as much as a launch.
+struct DeviceFacts {
+  int device, sms;
+  int32_t *status;      // the row-operator status word
+};
+cudaError_t device_facts(DeviceFacts *facts);
+
+// Raises a kernel's dynamic shared memory limit, once per kernel and device.
+template <typename Kernel>
+cudaError_t allow_shared(Kernel kernel, std::atomic<uint64_t> &done, int device, uint32_t bytes) {
+  if (device < 64 && (done.load(std::memory_order_acquire) >> device & 1)) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(bytes));
+  if (e == cudaSuccess && device < 64) done.fetch_or(uint64_t(1) << device, std::memory_order_release);
+  return e;
+}
 
 // Tiled tensor map (rank <= 5, element strides 1) over device memory; `swizzle`
 // is the swizzle width in bytes (0, 32, 64 or 128), `elt` the element size in

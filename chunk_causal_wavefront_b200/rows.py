@@ -13,15 +13,23 @@ them while gradients are recorded.
 from __future__ import annotations
 
 import contextlib
+import ctypes
+import struct
 from typing import Optional, Tuple, Union
 
 import torch
 
 from . import wf as _wf
-from .wf import WfError, WfRows
+from .wf import WfError
 
 _TYPES = {torch.bfloat16: _wf.WF_DTYPE_BF16, torch.float32: _wf.WF_DTYPE_F32}
 _ACTS = {"none": _wf.WF_ACT_NONE, "gelu": _wf.WF_ACT_GELU, "silu": _wf.WF_ACT_SILU}
+
+
+_NO_GRAD = "row operators compute no gradients: call them under torch.no_grad()"
+# The current stream's handle without a Stream object around it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 class E4M3Rows:
@@ -51,9 +59,13 @@ class E4M3Rows:
 
     @classmethod
     def empty(cls, rows: int, cols: int, device) -> "E4M3Rows":
-        n = _wf.wf_scale_bytes(rows, cols)
-        return cls(torch.empty(rows, cols, dtype=torch.float8_e4m3fn, device=device),
-                   torch.empty(n, dtype=torch.uint8, device=device))
+        if cols % 32 or cols <= 0:
+            raise ValueError("E4M3 rows need a multiple of 32 columns")
+        self = cls.__new__(cls)
+        self.codes = torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=device)
+        self.scales = torch.empty((rows + 127) // 128 * ((cols + 127) // 128) * 512,
+                                  dtype=torch.uint8, device=device)
+        return self
 
     @property
     def shape(self) -> torch.Size:
@@ -70,44 +82,63 @@ class E4M3Rows:
     def dequantize(self, out: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.bfloat16,
                    stream=None) -> torch.Tensor:
         """The values these rows stand for, as bf16 or fp32 (exact in both)."""
-        with _on(stream, (self,), (out,)) as raw:
+        with _on(stream, self, out) as raw:
             if out is None:
                 out = torch.empty(self.codes.shape, dtype=dtype, device=self.codes.device)
-            _check(_wf.wf_dequantize_rows(_rows(self), _rows(out), raw), "wf_dequantize_rows")
+            _check(_dequantize(_rows(self), _rows(out), raw), "wf_dequantize_rows")
         return out
 
 
 Operand = Union[torch.Tensor, E4M3Rows]
 
 
-def _rows(t: Optional[Operand]) -> Optional[WfRows]:
-    """The C description of rows; a view, never a copy."""
+# One wf_rows struct (native alignment, padded to its size).
+_pack = struct.Struct("PPqqqi0q").pack
+_E4M3 = _wf.WF_DTYPE_FP8_E4M3
+
+
+def _rows(t: Optional[Operand]) -> Optional[bytes]:
+    """The wf_rows struct of an operand, as bytes; a view, never a copy."""
     if t is None:
         return None
-    if isinstance(t, E4M3Rows):
+    if type(t) is E4M3Rows:
         c = t.codes
-        if c.stride(1) != 1:
-            raise ValueError("rows must have unit column stride")
         rows, cols = c.shape
-        ld = c.stride(0) if rows > 1 else max(c.stride(0), cols)
-        return WfRows(c.data_ptr() or None, t.scales.data_ptr() or None, rows, cols, ld,
-                      _wf.WF_DTYPE_FP8_E4M3)
+        ld, unit = c.stride()
+        if unit != 1 or (rows > 1 and ld < cols):
+            raise ValueError("rows must have unit column stride and not share memory")
+        return _pack(c.data_ptr(), t.scales.data_ptr(), rows, cols, ld if ld > cols else cols, _E4M3)
     code = _TYPES.get(t.dtype)
     if code is None:
         raise ValueError(f"rows must be bfloat16, float32 or E4M3Rows, not {t.dtype}")
-    if t.dim() == 0 or t.shape[-1] == 0:
+    shape = t.shape
+    cols = shape[-1] if shape else 0
+    if cols == 0:
         raise ValueError("rows must have at least one column")
-    cols = t.shape[-1]
     if t.is_contiguous():
-        rows, ld = t.numel() // cols, cols
-    elif t.dim() == 2 and (t.stride(1) == 1 or cols == 1):
-        rows, ld = t.shape[0], t.stride(0)
+        return _pack(t.data_ptr(), 0, t.numel() // cols, cols, cols, code)
+    if len(shape) == 2 and (t.stride(1) == 1 or cols == 1):
+        rows, ld = shape[0], t.stride(0)
         if rows > 1 and ld < cols:
             raise ValueError("rows that share memory (an expanded tensor) are not supported")
-        ld = max(ld, cols)
-    else:
-        raise ValueError("rows must be contiguous, or 2-D with unit column stride")
-    return WfRows(t.data_ptr() or None, None, rows, cols, ld, code)
+        return _pack(t.data_ptr(), 0, rows, cols, max(ld, cols), code)
+    raise ValueError("rows must be contiguous, or 2-D with unit column stride")
+
+
+def _entry(name: str):
+    """The library's entry point, taking wf_rows structs as bytes: building a ctypes
+    Structure for each operand costs more than the launch."""
+    fn = _wf.lib()[name]
+    P = ctypes.c_void_p
+    kinds = {"r": ctypes.c_char_p, "p": P, "i": ctypes.c_int32, "f": ctypes.c_float}
+    fn.argtypes = [kinds[k] for k in {"wf_quantize_rows": "rrp", "wf_dequantize_rows": "rrp",
+                                      "wf_add_rms_norm": "rrpfrrp", "wf_linear": "rrpirrp"}[name]]
+    fn.restype = ctypes.c_int32
+    return fn
+
+
+_quantize, _dequantize = _entry("wf_quantize_rows"), _entry("wf_dequantize_rows")
+_norm, _linear = _entry("wf_add_rms_norm"), _entry("wf_linear")
 
 
 def _check(status: int, what: str) -> None:
@@ -140,24 +171,22 @@ class _Here:
         return False
 
 
-def _on(stream, inputs, outputs):
+def _on(stream, x, *others):
     """Checks that everything is on one CUDA device and makes it current; gives the raw stream."""
-    device = None
+    device = x.device
+    if device.type != "cuda":
+        raise ValueError("row operators need CUDA tensors")
     grad = torch.is_grad_enabled()
-    for t in inputs + outputs:
-        if t is None:
-            continue
-        d = t.device
-        if device is None:
-            device = d
-            if d.type != "cuda":
-                raise ValueError("row operators need CUDA tensors")
-        elif d != device:
-            raise ValueError(f"all tensors must be on one device: got {device} and {d}")
-        if grad and not isinstance(t, E4M3Rows) and t.requires_grad:
-            raise ValueError("row operators compute no gradients: call them under torch.no_grad()")
+    if grad and type(x) is not E4M3Rows and x.requires_grad:
+        raise ValueError(_NO_GRAD)
+    for t in others:
+        if t is not None:
+            if t.device != device:
+                raise ValueError(f"all tensors must be on one device: got {device} and {t.device}")
+            if grad and type(t) is not E4M3Rows and t.requires_grad:
+                raise ValueError(_NO_GRAD)
     if stream is None and device.index == torch.cuda.current_device():
-        return _Here(torch.cuda.current_stream(device).cuda_stream)
+        return _Here(_raw_stream(device.index))
     if stream is not None and stream.device != device:
         raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
     return _scope(device, stream)
@@ -197,9 +226,9 @@ def _result(out: Optional[Operand], shape, out_dtype, default: torch.dtype, devi
 
 def quantize_rows(x: torch.Tensor, out: Optional[E4M3Rows] = None, stream=None) -> E4M3Rows:
     """x [..., cols] in bf16 or fp32 as E4M3 rows (leading dimensions flattened)."""
-    with _on(stream, (x,), (out,)) as raw:
+    with _on(stream, x, out) as raw:
         out = _result(out, x.shape, "e4m3" if out is None else None, x.dtype, x.device)
-        _check(_wf.wf_quantize_rows(_rows(x), _rows(out), raw), "wf_quantize_rows")
+        _check(_quantize(_rows(x), _rows(out), raw), "wf_quantize_rows")
     return out
 
 
@@ -219,12 +248,12 @@ def add_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *,
         raise ValueError(f"residual has shape {tuple(residual.shape)}, x {tuple(x.shape)}")
     if sum_out is not None and sum_out.shape != x.shape:
         raise ValueError(f"sum_out has shape {tuple(sum_out.shape)}, x {tuple(x.shape)}")
-    with _on(stream, (x, weight, residual), (out, sum_out)) as raw:
+    with _on(stream, x, weight, residual, out, sum_out) as raw:
         w = _vector(weight, x.shape[-1], "weight")
         out = _result(out, x.shape, out_dtype, x.dtype, x.device)
         if residual is not None and sum_out is None:
             sum_out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        _check(_wf.wf_add_rms_norm(_rows(x), _rows(residual), w, eps, _rows(sum_out),
+        _check(_norm(_rows(x), _rows(residual), w, eps, _rows(sum_out),
                                    _rows(out), raw), "wf_add_rms_norm")
     return out if residual is None else (out, sum_out)
 
@@ -246,10 +275,10 @@ def linear(x: Operand, w: Operand, bias: Optional[torch.Tensor] = None, *, act: 
     shape = tuple(x.shape[:-1]) + (w.shape[0],)
     if residual is not None and tuple(residual.shape) != shape:
         raise ValueError(f"residual has shape {tuple(residual.shape)}, not {shape}")
-    with _on(stream, (x, w, bias, residual), (out,)) as raw:
+    with _on(stream, x, w, bias, residual, out) as raw:
         b = _vector(bias, w.shape[0], "bias")
         out = _result(out, shape, out_dtype, torch.bfloat16, x.device)
-        _check(_wf.wf_linear(_rows(x), _rows(w), b, _ACTS[act], _rows(residual), _rows(out),
+        _check(_linear(_rows(x), _rows(w), b, _ACTS[act], _rows(residual), _rows(out),
                              raw), "wf_linear")
     return out
 

@@ -459,8 +459,12 @@ def test_refusals_on_device():
     with pytest.raises(wfb.WfError) as e:
         wfb.linear(wfb.quantize_rows(x), w)
     assert e.value.status == W.WF_ERR_UNSUPPORTED
-    with pytest.raises(wfb.WfError):
+    with pytest.raises(ValueError, match="32"):
         wfb.quantize_rows(rows(4, 48, 93))
+    shared = wfb.E4M3Rows(torch.zeros(1, 64, device="cuda").to(torch.float8_e4m3fn).expand(4, 64),
+                          torch.zeros(512, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError, match="share"):
+        shared.dequantize()
     y = wfb.linear(x[:0], w)
     assert y.shape == (0, 8)
     assert wfb.add_rms_norm(x[:0]).shape == (0, 64)

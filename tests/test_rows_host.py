@@ -187,11 +187,11 @@ def test_binding_refusals_on_cpu_tensors():
 
 def test_row_descriptions():
     x = torch.zeros(2, 3, 64, dtype=torch.bfloat16)
-    r = PR._rows(x)
+    r = W.WfRows.from_buffer_copy(PR._rows(x))
     assert (r.rows, r.cols, r.ld, r.dtype) == (6, 64, 64, BF16)
-    r = PR._rows(torch.zeros(5, 96)[:, :64])
+    r = W.WfRows.from_buffer_copy(PR._rows(torch.zeros(5, 96)[:, :64]))
     assert (r.rows, r.cols, r.ld, r.dtype) == (5, 64, 96, F32)
-    r = PR._rows(torch.zeros(64, dtype=torch.bfloat16))
+    r = W.WfRows.from_buffer_copy(PR._rows(torch.zeros(64, dtype=torch.bfloat16)))
     assert (r.rows, r.cols) == (1, 64)
     for bad in (torch.zeros(4, 64).t(), torch.zeros(2, 3, 64)[:, :, ::2], torch.zeros(1, 64).expand(4, 64),
                 torch.zeros(4, 0), torch.zeros(()), torch.zeros(4, 64, dtype=torch.float16)):
