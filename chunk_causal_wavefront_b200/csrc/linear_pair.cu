@@ -15,11 +15,11 @@
 // Tiles are walked in groups of 8 row tiles, feature tiles slowest inside a
 // group, so that the tiles in flight cover a near-square patch of the output and
 // both operands are re-read from L2.
-//   warp 8             TMA producer of its CTA (128-byte swizzled operand boxes,
+//   producer warp      TMA producer of its CTA (128-byte swizzled operand boxes,
 //                      for E4M3 also the 512-byte scale tiles: one of x, and two
 //                      that cover the BN features of w in both CTAs); all bytes
 //                      count on the leader's full barrier.
-//   warp 9             leader only: copies the stage's scales into TMEM, then
+//   MMA warp           leader only: copies the stage's scales into TMEM, then
 //                      issues the MMAs; k-steps past K are not issued, so scale
 //                      bytes past the last block are never used.
 //   Both run as whole warps that elect a lane for each stage: with a branch on the
@@ -27,7 +27,7 @@
 //   through registers, about 140 cycles apiece, and the issue bounds the kernel
 //   (4680 x 20480 x 5120 bf16 716 us against 668, 23400 x 1536 x 6144 E4M3 228
 //   against 187).
-//   warps 0-7          epilogue: warpgroup e takes columns [e BN/2, (e+1) BN/2)
+//   the other warps    epilogue: a warpgroup takes 64 (BN = 192) or 128 columns
 //                      of the CTA's 128 rows, a thread owns one row and 32
 //                      columns at a time. The residual's 32 x 32 box comes in by
 //                      TMA one step ahead into the staging buffer that the result
@@ -48,10 +48,6 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kThreads = 320;
-constexpr int kEpiWarps = 8;
-constexpr int kProducerWarp = 8;
-constexpr int kMmaWarp = 9;
 constexpr int kBufs = 3;                        // staging buffers per epilogue warp
 constexpr uint32_t kBufBytes = 32 * 64;         // 32 rows x 32 bf16 columns
 constexpr int kGroup = 8;                       // row tiles per raster group
@@ -63,7 +59,14 @@ struct Shape {
   static constexpr uint32_t kBBytes = BN / 2 * 128;
   static constexpr uint32_t kScaleBytes = MX ? 512 + 1024 : 0;
   static constexpr uint32_t kStageBytes = kABytes + kBBytes + kScaleBytes;   // per CTA
-  static constexpr int kStages = MX || BN == 256 ? 5 : 6;
+  static constexpr int kStages = 5;
+  // Epilogue: warpgroups of kCols columns. Three at BN = 192 (registers allow no
+  // more at 256, where the accumulator's columns are shared by two).
+  static constexpr int kCols = BN == 192 ? 64 : 128;
+  static constexpr int kEpiWarps = BN / kCols * 4;
+  static constexpr int kProducerWarp = kEpiWarps;
+  static constexpr int kMmaWarp = kEpiWarps + 1;
+  static constexpr int kThreads = 32 * (kEpiWarps + 2);
   static constexpr int kKElems = MX ? 128 : 64;        // elements of a k-block
   static constexpr int kKStep = MX ? 32 : 16;          // elements per MMA
   // Operands of all stages first (1024-byte aligned for the swizzle), then the
@@ -103,7 +106,7 @@ __device__ __forceinline__ void decode(const PairGrid &g, int t, int &mt, int &n
 }
 
 template <bool MX, int BN, bool OUT8>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MX, BN>::kThreads, 1)
     linear_pair_kernel(const __grid_constant__ LinearParams p, const __grid_constant__ PairGrid g,
                        const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw,
                        const __grid_constant__ CUtensorMap tsx, const __grid_constant__ CUtensorMap tsw,
@@ -124,10 +127,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tw);
     *abort_flag = 0;
     for (int b = 0; b < S::kNumBars; ++b)
-      mbar_init(bars + b, (b == S::kAccEmpty0 || b == S::kAccEmpty0 + 1) ? 2 * kEpiWarps : 1);
+      mbar_init(bars + b, (b == S::kAccEmpty0 || b == S::kAccEmpty0 + 1) ? 2 * S::kEpiWarps : 1);
     fence_barrier_init();
   }
-  if (warp == kMmaWarp) {                   // same warp in both CTAs, same slot offset
+  if (warp == S::kMmaWarp) {                   // same warp in both CTAs, same slot offset
     tmem_alloc_pair(tmem_slot, 512);
     tmem_relinquish_pair();
   }
@@ -137,7 +140,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const Ctx ctx{bars, abort_flag, p.status};
 
-  if (warp == kProducerWarp) {
+  if (warp == S::kProducerWarp) {
     // ------------------------------------------------------------ producer --
     int q = 0;                              // k-blocks issued by this CTA
     bool ok = true;
@@ -172,7 +175,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int fills = q / S::kStages + (s < q % S::kStages ? 1 : 0);
       if (fills > 0) drain_wait(ctx, S::kEmpty0 + s, (fills - 1) & 1);
     }
-  } else if (warp == kMmaWarp) {
+  } else if (warp == S::kMmaWarp) {
     // ---------------------------------------------------------- MMA issuer --
     if (rank == 0) {
       const uint32_t hi = desc_hi_sw128(1024);
@@ -234,8 +237,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ epilogue --
-    constexpr int kSteps = BN / 64;                      // 32-column steps of a warpgroup
-    const int e = warp >> 2;                             // column half of the tile
+    constexpr int kSteps = S::kCols / 32;                // 32-column steps of a warpgroup
+    const int e = warp >> 2;                             // warpgroup: kCols columns of the tile
     const int wr = (warp & 3) * 32;                      // first row of this warp
     const uint32_t lane_addr = static_cast<uint32_t>(wr) << 16;
     uint8_t *bufs = smem + S::kOffBuf + warp * kBufs * kBufBytes;
@@ -248,7 +251,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int mt, nt;
       decode(g, t, mt, nt);
       row0 = mt * 256 + static_cast<int>(rank) * 128 + wr;
-      col0 = nt * BN + e * (BN / 2) + c * 32;
+      col0 = nt * BN + e * S::kCols + c * 32;
       return row0 < p.M && col0 < p.N;
     };
     auto fetch = [&](int t, int c, int buf) {            // lane 0: residual box of a step
@@ -275,7 +278,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ok = __all_sync(0xffffffffu, wait_bar_cluster(ctx, S::kAccFull0 + b, (i >> 1) & 1));
       if (!ok) break;
       tc_fence_after();
-      const uint32_t tcol = tmem + lane_addr + BN * b + e * (BN / 2);
+      const uint32_t tcol = tmem + lane_addr + BN * b + e * S::kCols;
       uint32_t cur[32], nxt[32];
       tmem_ld32(tcol, cur);
       tmem_ld_wait();
@@ -313,14 +316,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = activate(v[j], kSilu);
           }
-          uint8_t *stage = bufs + buf * kBufBytes;
+          // Staging rows of 64 bytes, 64-byte swizzle: 16-byte chunk j of row r at
+          // j ^ (r / 2 % 4).
+          const uint32_t addr = smem_u32(bufs + buf * kBufBytes + lane * 64);
+          const uint32_t x = (lane >> 1) & 3;
           if constexpr (OUT8) {
+            // The warpgroup's 64 columns share a staging row: two scale blocks.
             float m = 0.f;
 #pragma unroll
             for (int j = 0; j < 32; ++j) m = fmaxf(m, fabsf(v[j]));
             const int ex = block_exponent(m);
             const float f = block_factor(ex);
-            const uint32_t addr = smem_u32(stage + lane * 32);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               uint32_t w[4];
@@ -329,7 +335,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const float *u = v + 16 * j + 4 * h;
                 w[h] = pack_e4m3x4(u[0] * f, u[1] * f, u[2] * f, u[3] * f);
               }
-              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr + 16 * j),
+              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr + (((2 * c + j) ^ x) << 4)),
                            "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
                            : "memory");
             }
@@ -337,9 +343,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               p.out.scales[scale_offset(row0 + lane, col0 >> 5, g.out_block_tiles)] =
                   static_cast<uint8_t>(ex + 127);
           } else {
-            // 64-byte rows, 64-byte swizzle: 16-byte chunk j of row r at j ^ (r / 2 % 4).
-            const uint32_t addr = smem_u32(stage + lane * 64);
-            const uint32_t x = (lane >> 1) & 3;
             if (g.has_residual) {
               ok = __all_sync(0xffffffffu, wait_bar(ctx, res_bar + buf, (res_phase >> buf) & 1));
               if (!ok) break;
@@ -374,11 +377,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           fence_proxy_async_smem();
         }
         __syncwarp();
-        if (lane == 0) {
-          if (on) tma_store_2d(&to, bufs + buf * kBufBytes, col0, row0);
-          tma_store_commit();                            // a group per step, empty or not
+        if constexpr (OUT8) {
+          // One store for both steps; columns past N are clipped.
+          if (c + 1 == kSteps) {
+            if (lane == 0) {
+              if (place(t, 0, row0, col0)) tma_store_2d(&to, bufs + buf * kBufBytes, col0, row0);
+              tma_store_commit();
+            }
+            buf = buf1;
+          }
+        } else {
+          if (lane == 0) {
+            if (on) tma_store_2d(&to, bufs + buf * kBufBytes, col0, row0);
+            tma_store_commit();                          // a group per step, empty or not
+          }
+          buf = buf1;
         }
-        buf = buf1;
         if (c + 1 < kSteps) {
           tmem_ld_wait();
           reg_fence32(nxt);
@@ -405,7 +419,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncwarp();
   tc_fence_before();
   cluster_sync();                           // no MMA or load of the pair is in flight
-  if (warp == kMmaWarp) {
+  if (warp == S::kMmaWarp) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);
   }
@@ -419,7 +433,7 @@ cudaError_t run_pair(const LinearParams &p, cudaStream_t st) {
   const uint64_t K = static_cast<uint64_t>(p.K), M = static_cast<uint64_t>(p.M), N = static_cast<uint64_t>(p.N);
   const uint64_t xd[2] = {K, M}, wd[2] = {K, N}, od[2] = {N, M};
   const uint64_t xs[1] = {static_cast<uint64_t>(p.x.ld) * elt}, ws[1] = {static_cast<uint64_t>(p.w.ld) * elt};
-  const uint32_t xb[2] = {S::kKElems, 128}, wb[2] = {S::kKElems, BN / 2}, ob[2] = {32, 32};
+  const uint32_t xb[2] = {S::kKElems, 128}, wb[2] = {S::kKElems, BN / 2}, ob[2] = {OUT8 ? 64 : 32, 32};
   bool ok = encode_rows_map(&tx, elt, 128, p.x.data, 2, xd, xs, xb) &&
             encode_rows_map(&tw, elt, 128, p.w.data, 2, wd, ws, wb);
   if (MX) {
@@ -433,7 +447,7 @@ cudaError_t run_pair(const LinearParams &p, cudaStream_t st) {
   }
   const int oelt = OUT8 ? 1 : 2;
   const uint64_t os[1] = {static_cast<uint64_t>(p.out.ld) * oelt};
-  ok = ok && encode_rows_map(&to, oelt, OUT8 ? 0 : 64, p.out.data, 2, od, os, ob);
+  ok = ok && encode_rows_map(&to, oelt, 64, p.out.data, 2, od, os, ob);
   if (p.residual.data) {
     const uint64_t rs[1] = {static_cast<uint64_t>(p.residual.ld) * 2};
     ok = ok && encode_rows_map(&tr, 2, 64, p.residual.data, 2, od, rs, ob);
@@ -453,7 +467,7 @@ cudaError_t run_pair(const LinearParams &p, cudaStream_t st) {
   const cudaError_t e = allow_shared(linear_pair_kernel<MX, BN, OUT8>, allowed, p.device, S::kSmemBytes);
   if (e != cudaSuccess) return e;
   const int pairs = g.total < p.sms / 2 ? g.total : p.sms / 2;
-  linear_pair_kernel<MX, BN, OUT8><<<2 * pairs, kThreads, S::kSmemBytes, st>>>(p, g, tx, tw, tsx, tsw, tr, to);
+  linear_pair_kernel<MX, BN, OUT8><<<2 * pairs, S::kThreads, S::kSmemBytes, st>>>(p, g, tx, tw, tsx, tsw, tr, to);
   return cudaGetLastError();
 }
 
@@ -461,8 +475,8 @@ cudaError_t run_pair(const LinearParams &p, cudaStream_t st) {
 
 cudaError_t launch_linear_pair(const LinearParams &p, bool e4m3, bool out_e4m3, int bn, cudaStream_t st) {
   if (e4m3) return out_e4m3 ? run_pair<true, 192, true>(p, st) : run_pair<true, 192, false>(p, st);
-  if (bn == 256) return out_e4m3 ? run_pair<false, 256, true>(p, st) : run_pair<false, 256, false>(p, st);
-  return out_e4m3 ? run_pair<false, 192, true>(p, st) : run_pair<false, 192, false>(p, st);
+  if (out_e4m3) return run_pair<false, 192, true>(p, st);
+  return bn == 256 ? run_pair<false, 256, false>(p, st) : run_pair<false, 192, false>(p, st);
 }
 
 }  // namespace wf

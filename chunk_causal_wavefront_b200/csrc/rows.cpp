@@ -133,6 +133,58 @@ wf_status convert(const wf_rows *x, const wf_rows *out, bool to_e4m3, cudaStream
                            : launch_dequantize_rows(p, type_of(out->dtype), st));
 }
 
+// Which kernel a product takes, and its tile: the smallest estimate of the time in
+// microseconds, from figures measured on a B200 at 1965 MHz with weights in HBM.
+struct Plan {
+  bool pair;
+  int bn, nt, split;
+};
+
+Plan plan_linear(const LinearParams &p, bool e4m3, bool stored_by_tma) {
+  const int64_t n_kb = (static_cast<int64_t>(p.K) + (e4m3 ? 127 : 63)) / (e4m3 ? 128 : 64);
+  const auto tiles = [](int64_t n, int64_t by) { return (n + by - 1) / by; };
+  Plan best{false, 0, 0, 0};
+  double least = 0.0;
+  const auto offer = [&](double us, const Plan &plan) {
+    if (best.nt == 0 && !best.pair) least = us + 1.0;
+    if (us < least) {
+      least = us;
+      best = plan;
+    }
+  };
+  if (stored_by_tma) {
+    // Waves of CTA pairs: a k-block of 128 bytes takes 0.26 (192 features) or
+    // 0.34 us (256), a tile no less than its epilogue's 2.5 us.
+    for (int bn = 192; bn <= (e4m3 ? 192 : 256); bn += 64) {
+      const double k_block = bn == 192 ? 0.26 : 0.34;
+      const int64_t waves = tiles(tiles(p.M, 256) * tiles(p.N, bn), p.sms / 2);
+      const double tile = n_kb * k_block;
+      offer(7.0 + waves * (tile > 2.5 ? tile : 2.5), Plan{true, bn, 0, 0});
+    }
+  }
+  // Features on the M side: either the chain of k-blocks of a CTA (two CTAs per SM
+  // up to 64 tokens) and its epilogue, or the bytes that all tiles read through L2
+  // at 11 TB/s, or the weights from HBM.
+  for (int nt = 16; nt <= 128; nt *= 2) {
+    // Several token tiles need 64-row steps of the E4M3 scale tiles, and 16-token
+    // tiles are for a single one.
+    if (p.M > nt && (nt == 16 || (e4m3 && nt < 64))) continue;
+    const double k_block = nt == 16 ? 0.20 : nt == 32 ? 0.25 : nt == 64 ? 0.33 : 0.40;
+    const int64_t all = tiles(p.N, 128) * tiles(p.M, nt);
+    const int64_t room = static_cast<int64_t>(p.sms) * (nt <= 64 ? 2 : 1);
+    for (int split = 1; split <= 8 && split <= n_kb; split *= 2) {
+      const double chain = static_cast<double>(tiles(n_kb, split)) * k_block + 0.05 * nt / split;
+      double us = tiles(all * split, room) * chain;
+      const double l2 = all * n_kb * (16.0 + nt / 8.0) / 11e3, hbm = p.N * 128e-3 * n_kb / 6.5e3;
+      us = us > l2 ? us : l2;
+      us = us > hbm ? us : hbm;
+      offer(4.0 + us + (split == 8 ? 0.5 : 0.0), Plan{false, 0, nt, split});
+    }
+    if (p.M <= nt) break;
+  }
+  return best;
+}
+
 bool rows16(const wf_rows *r) {
   return multiple_of(r->data, 16) && row_stride(r) * element_size(r->dtype) % 16 == 0;
 }
@@ -227,21 +279,9 @@ wf_status wf_linear(const wf_rows *x, const wf_rows *w, const float *bias, int32
   p.sms = dev.sms;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool stored_by_tma = rows16(out) && (!residual || rows16(residual));
-  const int sms = dev.sms;
-  const int64_t m_tiles = (x->rows + 255) / 256;
-  if (stored_by_tma && x->rows > 128 && m_tiles * ((w->rows + 191) / 192) >= sms / 4) {
-    // Waves of CTA pairs times the tile's width: what the last wave wastes.
-    const int64_t pairs = sms / 2;
-    const int64_t w192 = (m_tiles * ((w->rows + 191) / 192) + pairs - 1) / pairs * 192;
-    const int64_t w256 = (m_tiles * ((w->rows + 255) / 256) + pairs - 1) / pairs * 256;
-    return status_of(launch_linear_pair(p, e4m3, out8, w256 <= w192 ? 256 : 192, st));
-  }
-  const int nt = x->rows <= 16 ? 16 : x->rows <= 32 ? 32 : x->rows <= 64 ? 64 : 128;
-  const int64_t tiles = (w->rows + 127) / 128 * ((x->rows + nt - 1) / nt);
-  const int64_t n_kb = e4m3 ? (x->cols + 127) / 128 : (x->cols + 63) / 64;
-  int split = 1;
-  while (split < 8 && tiles * split < sms && n_kb >= 4 * split) split *= 2;
-  return status_of(launch_linear_skinny(p, e4m3, out8, nt, split, st));
+  const Plan plan = plan_linear(p, e4m3, stored_by_tma);
+  return status_of(plan.pair ? launch_linear_pair(p, e4m3, out8, plan.bn, st)
+                             : launch_linear_skinny(p, e4m3, out8, plan.nt, plan.split, st));
 }
 
 wf_status wf_rows_check_status(wf_stream_t stream) {

@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 import struct
 from typing import Optional, Tuple, Union
 
@@ -59,13 +60,9 @@ class E4M3Rows:
 
     @classmethod
     def empty(cls, rows: int, cols: int, device) -> "E4M3Rows":
-        if cols % 32 or cols <= 0:
-            raise ValueError("E4M3 rows need a multiple of 32 columns")
-        self = cls.__new__(cls)
-        self.codes = torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=device)
-        self.scales = torch.empty((rows + 127) // 128 * ((cols + 127) // 128) * 512,
-                                  dtype=torch.uint8, device=device)
-        return self
+        n = _wf.wf_scale_bytes(rows, cols)
+        return cls(torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=device),
+                   torch.empty(n, dtype=torch.uint8, device=device))
 
     @property
     def shape(self) -> torch.Size:
@@ -82,10 +79,13 @@ class E4M3Rows:
     def dequantize(self, out: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.bfloat16,
                    stream=None) -> torch.Tensor:
         """The values these rows stand for, as bf16 or fp32 (exact in both)."""
-        with _on(stream, self, out) as raw:
-            if out is None:
-                out = torch.empty(self.codes.shape, dtype=dtype, device=self.codes.device)
-            _check(_dequantize(_rows(self), _rows(out), raw), "wf_dequantize_rows")
+        raw = _here(stream, self, out)
+        if raw is None:
+            with _elsewhere(self.device, stream):
+                return self.dequantize(out, dtype)
+        if out is None:
+            out = self.codes.new_empty(self.codes.shape, dtype=dtype)
+        _check(_dequantize(_rows(self), _rows(out), raw), "wf_dequantize_rows")
         return out
 
 
@@ -146,33 +146,9 @@ def _check(status: int, what: str) -> None:
         raise WfError(status, what)
 
 
-@contextlib.contextmanager
-def _scope(device, stream):
-    with torch.cuda.device(device):
-        if stream is None:
-            yield torch.cuda.current_stream(device).cuda_stream
-        else:
-            with torch.cuda.stream(stream):   # outputs allocated here belong to the stream
-                yield stream.cuda_stream
-
-
-class _Here:
-    """The common case of _on: the tensors' device is current, no stream given."""
-
-    __slots__ = ("raw",)
-
-    def __init__(self, raw):
-        self.raw = raw
-
-    def __enter__(self):
-        return self.raw
-
-    def __exit__(self, *exc):
-        return False
-
-
-def _on(stream, x, *others):
-    """Checks that everything is on one CUDA device and makes it current; gives the raw stream."""
+def _here(stream, x, *others) -> Optional[int]:
+    """Checks that everything is on one CUDA device. The raw current stream if that device is
+    current and no stream is given; else None: the call goes through _elsewhere."""
     device = x.device
     if device.type != "cuda":
         raise ValueError("row operators need CUDA tensors")
@@ -185,50 +161,65 @@ def _on(stream, x, *others):
                 raise ValueError(f"all tensors must be on one device: got {device} and {t.device}")
             if grad and type(t) is not E4M3Rows and t.requires_grad:
                 raise ValueError(_NO_GRAD)
-    if stream is None and device.index == torch.cuda.current_device():
-        return _Here(_raw_stream(device.index))
-    if stream is not None and stream.device != device:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-    return _scope(device, stream)
-
-
-def _vector(v: Optional[torch.Tensor], n: int, name: str) -> Optional[int]:
-    if v is None:
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
         return None
+    index = device.index
+    return _raw_stream(index) if index == torch.cuda.current_device() else None
+
+
+@contextlib.contextmanager
+def _elsewhere(device, stream):
+    """Makes the tensors' device current, and the given stream, so that outputs allocated
+    inside belong to it."""
+    with torch.cuda.device(device):
+        if stream is None:
+            yield
+        else:
+            with torch.cuda.stream(stream):
+                yield
+
+
+def _vector(v: torch.Tensor, n: int, name: str) -> int:
     if v.dtype != torch.float32 or v.shape != (n,) or not v.is_contiguous():
         raise ValueError(f"{name} must be a contiguous float32 vector of {n} elements")
     return v.data_ptr()
 
 
-def _result(out: Optional[Operand], shape, out_dtype, default: torch.dtype, device) -> Operand:
-    """The caller's output after a check of its shape, or a new one."""
-    if out is not None:
-        if out_dtype is not None:
-            raise ValueError("give out or out_dtype, not both")
-        want = tuple(shape)
-        if isinstance(out, E4M3Rows):
-            n = 1
-            for s in want[:-1]:
-                n *= s
-            want = (n, want[-1])
-        if tuple(out.shape) != want:
-            raise ValueError(f"out has shape {tuple(out.shape)}, not {want}")
-        return out
+def _given(out: Operand, shape, out_dtype) -> Operand:
+    """The caller's output after a check of its shape (E4M3 rows: leading dimensions flattened)."""
+    if out_dtype is not None:
+        raise ValueError("give out or out_dtype, not both")
+    want = (math.prod(shape[:-1]), shape[-1]) if isinstance(out, E4M3Rows) else tuple(shape)
+    if tuple(out.shape) != want:
+        raise ValueError(f"out has shape {tuple(out.shape)}, not {want}")
+    return out
+
+
+def _new(like: torch.Tensor, shape, out_dtype, default: torch.dtype) -> Operand:
+    """A new output on the device of `like`."""
+    if out_dtype is None or out_dtype is default:
+        return like.new_empty(shape, dtype=default)
     if out_dtype == "e4m3":
-        rows = 1
-        for s in shape[:-1]:
-            rows *= s
-        return E4M3Rows.empty(rows, shape[-1], device)
-    if out_dtype is not None and out_dtype is not default:
-        raise ValueError(f"out_dtype must be {default} (the default) or 'e4m3'")
-    return torch.empty(shape, dtype=default, device=device)
+        rows, cols = math.prod(shape[:-1]), shape[-1]
+        if cols % 32:
+            raise ValueError("E4M3 rows need a multiple of 32 columns")
+        out = E4M3Rows.__new__(E4M3Rows)
+        out.codes = like.new_empty((rows, cols), dtype=torch.float8_e4m3fn)
+        out.scales = like.new_empty((rows + 127) // 128 * ((cols + 127) // 128) * 512, dtype=torch.uint8)
+        return out
+    raise ValueError(f"out_dtype must be {default} (the default) or 'e4m3'")
 
 
 def quantize_rows(x: torch.Tensor, out: Optional[E4M3Rows] = None, stream=None) -> E4M3Rows:
     """x [..., cols] in bf16 or fp32 as E4M3 rows (leading dimensions flattened)."""
-    with _on(stream, x, out) as raw:
-        out = _result(out, x.shape, "e4m3" if out is None else None, x.dtype, x.device)
-        _check(_quantize(_rows(x), _rows(out), raw), "wf_quantize_rows")
+    raw = _here(stream, x, out)
+    if raw is None:
+        with _elsewhere(x.device, stream):
+            return quantize_rows(x, out)
+    out = _new(x, x.shape, "e4m3", x.dtype) if out is None else _given(out, x.shape, None)
+    _check(_quantize(_rows(x), _rows(out), raw), "wf_quantize_rows")
     return out
 
 
@@ -242,20 +233,29 @@ def add_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *,
     E4M3Rows with out_dtype="e4m3" (or out=E4M3Rows). sum_out may be x or
     residual: the residual stream is then updated in place. weight is float32.
     """
-    if residual is None and sum_out is not None:
-        raise ValueError("sum_out needs a residual")
-    if residual is not None and residual.shape != x.shape:
-        raise ValueError(f"residual has shape {tuple(residual.shape)}, x {tuple(x.shape)}")
-    if sum_out is not None and sum_out.shape != x.shape:
-        raise ValueError(f"sum_out has shape {tuple(sum_out.shape)}, x {tuple(x.shape)}")
-    with _on(stream, x, weight, residual, out, sum_out) as raw:
-        w = _vector(weight, x.shape[-1], "weight")
-        out = _result(out, x.shape, out_dtype, x.dtype, x.device)
-        if residual is not None and sum_out is None:
-            sum_out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        _check(_norm(_rows(x), _rows(residual), w, eps, _rows(sum_out),
-                                   _rows(out), raw), "wf_add_rms_norm")
-    return out if residual is None else (out, sum_out)
+    shape = x.shape
+    if residual is None:
+        if sum_out is not None:
+            raise ValueError("sum_out needs a residual")
+    elif residual.shape != shape:
+        raise ValueError(f"residual has shape {tuple(residual.shape)}, x {tuple(shape)}")
+    if sum_out is not None and sum_out.shape != shape:
+        raise ValueError(f"sum_out has shape {tuple(sum_out.shape)}, x {tuple(shape)}")
+    raw = _here(stream, x, weight, residual, out, sum_out)
+    if raw is None:
+        with _elsewhere(x.device, stream):
+            return add_rms_norm(x, weight, residual=residual, eps=eps, out=out, sum_out=sum_out,
+                                out_dtype=out_dtype)
+    xr = _rows(x)
+    w = None if weight is None else _vector(weight, shape[-1], "weight")
+    out = _new(x, shape, out_dtype, x.dtype) if out is None else _given(out, shape, out_dtype)
+    if residual is None:
+        _check(_norm(xr, None, w, eps, None, _rows(out), raw), "wf_add_rms_norm")
+        return out
+    if sum_out is None:
+        sum_out = x.new_empty(shape)
+    _check(_norm(xr, _rows(residual), w, eps, _rows(sum_out), _rows(out), raw), "wf_add_rms_norm")
+    return out, sum_out
 
 
 def linear(x: Operand, w: Operand, bias: Optional[torch.Tensor] = None, *, act: str = "none",
@@ -268,18 +268,25 @@ def linear(x: Operand, w: Operand, bias: Optional[torch.Tensor] = None, *, act: 
     E4M3Rows with out_dtype="e4m3" (or out=E4M3Rows), then without a residual.
     out may be residual itself.
     """
-    if act not in _ACTS:
+    code = _ACTS.get(act)
+    if code is None:
         raise ValueError(f"act must be one of {sorted(_ACTS)}")
-    if len(w.shape) != 2 or len(x.shape) == 0 or x.shape[-1] != w.shape[1]:
-        raise ValueError(f"shapes {tuple(x.shape)} and {tuple(w.shape)} do not give x w^T")
-    shape = tuple(x.shape[:-1]) + (w.shape[0],)
-    if residual is not None and tuple(residual.shape) != shape:
+    xs, ws = x.shape, w.shape
+    if len(ws) != 2 or not xs or xs[-1] != ws[1]:
+        raise ValueError(f"shapes {tuple(xs)} and {tuple(ws)} do not give x w^T")
+    shape = (*xs[:-1], ws[0])
+    if residual is not None and residual.shape != shape:
         raise ValueError(f"residual has shape {tuple(residual.shape)}, not {shape}")
-    with _on(stream, x, w, bias, residual, out) as raw:
-        b = _vector(bias, w.shape[0], "bias")
-        out = _result(out, shape, out_dtype, torch.bfloat16, x.device)
-        _check(_linear(_rows(x), _rows(w), b, _ACTS[act], _rows(residual), _rows(out),
-                             raw), "wf_linear")
+    raw = _here(stream, x, w, bias, residual, out)
+    if raw is None:
+        with _elsewhere(x.device, stream):
+            return linear(x, w, bias, act=act, residual=residual, out=out, out_dtype=out_dtype)
+    b = None if bias is None else _vector(bias, ws[0], "bias")
+    if out is None:
+        out = _new(x.codes if type(x) is E4M3Rows else x, shape, out_dtype, torch.bfloat16)
+    else:
+        _given(out, shape, out_dtype)
+    _check(_linear(_rows(x), _rows(w), b, code, _rows(residual), _rows(out), raw), "wf_linear")
     return out
 
 
