@@ -4,10 +4,10 @@
 // All three read each element once and write each result once; HBM bounds them.
 //
 // Norm: s = x + residual, out = s / sqrt(mean(s^2) + eps) * weight.
-//   A row stays in registers between its one read and its one write: 1, 2, 4 or
-//   8 warps share a row, each lane holds up to four chunks of 8 elements (16-byte
-//   loads of bf16), all of a row's loads are issued before the first use, and
-//   the weight's chunks stay in registers over the rows that a block walks. The
+//   A row stays in registers between its one read and its one write: up to 8
+//   warps share a row, each lane holds up to four chunks of 8 elements (16-byte
+//   loads of bf16), and the next row's loads are issued before this row's sum is
+//   reduced. The weight comes from L1 (held in registers it cost occupancy). The
 //   sum of squares is fp32: per lane, then by shuffles, then over the row's warps
 //   through shared memory in a fixed order.
 //   E4M3 output: a block of 32 columns is four neighbouring lanes' chunks, so its
@@ -89,84 +89,81 @@ __device__ __forceinline__ float amax8(const float (&v)[8]) {
   return m;
 }
 
-// WPR warps per row, CH chunks of 8 elements per lane.
-template <typename T, bool OUT8, int WPR, int CH>
-__global__ void __launch_bounds__(kNormThreads)
-    norm_kernel(const NormParams p) {
-  constexpr int kRows = kNormThreads / 32 / WPR;   // rows per block and pass
+// CH chunks of 8 elements per lane; `wpr` warps per row, blockDim / 32 / wpr rows
+// per block and pass. The next pass's rows are loaded before this pass's sums
+// are reduced, so that loads are in flight at every barrier. Outputs may be the
+// inputs: a chunk is stored by the thread that loaded it, and rows do not overlap.
+template <typename T, bool OUT8, int CH>
+__global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormParams p, const int wpr) {
   __shared__ float part[2][kNormThreads / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int sub = warp / WPR;                      // row of the block's pass
-  const int t = (warp % WPR) * 32 + lane;          // thread of the row
-  const int chunks = p.cols >> 3;
+  const int sub = warp / wpr;                      // row of the block's pass
+  const int rows = blockDim.x / 32 / wpr;
+  const int t = (warp - sub * wpr) * 32 + lane;    // thread of the row
+  const int chunks = p.cols >> 3, stride = 32 * wpr;
   const float inv = 1.0f / static_cast<float>(p.cols);
-  float w[CH][8];
-#pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    const int k = t + c * 32 * WPR;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[c][i] = 1.0f;
-    if (p.weight && k < chunks) {
-      const float4 a = __ldg(reinterpret_cast<const float4 *>(p.weight) + 2 * k);
-      const float4 b = __ldg(reinterpret_cast<const float4 *>(p.weight) + 2 * k + 1);
-      w[c][0] = a.x; w[c][1] = a.y; w[c][2] = a.z; w[c][3] = a.w;
-      w[c][4] = b.x; w[c][5] = b.y; w[c][6] = b.z; w[c][7] = b.w;
-    }
-  }
   const int block_tiles = (p.cols + 127) >> 7;
-  int turn = 0;
-  for (int64_t base = static_cast<int64_t>(blockIdx.x) * kRows; base < p.rows;
-       base += static_cast<int64_t>(gridDim.x) * kRows, turn ^= 1) {
-    const int64_t row = base + sub;
-    const bool live = row < p.rows;
-    const T *x = static_cast<const T *>(p.x.data) + row * p.x.ld;
-    const T *r = p.residual.data ? static_cast<const T *>(p.residual.data) + row * p.residual.ld : nullptr;
-    typename RawOf<T>::type rx[CH], rr[CH];
+  const T *x = static_cast<const T *>(p.x.data), *r = static_cast<const T *>(p.residual.data);
+  typename RawOf<T>::type rx[CH] = {}, rr[CH] = {};
+  auto load = [&](int64_t row) {
+    if (row >= p.rows) return;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int k = t + c * 32 * WPR;
-      if (live && k < chunks) {
-        rx[c] = load8(x + 8 * k);
-        if (r) rr[c] = load8(r + 8 * k);
+      const int k = t + c * stride;
+      if (k < chunks) {
+        rx[c] = load8(x + row * p.x.ld + 8 * k);
+        if (r) rr[c] = load8(r + row * p.residual.ld + 8 * k);
       }
     }
+  };
+  const int64_t step = static_cast<int64_t>(gridDim.x) * rows;
+  int64_t base = static_cast<int64_t>(blockIdx.x) * rows;
+  load(base + sub);
+  for (int turn = 0; base < p.rows; base += step, turn ^= 1) {
+    const int64_t row = base + sub;
+    const bool live = row < p.rows;
     float v[CH][8];
     float ss = 0.f;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const bool on = live && t + c * 32 * WPR < chunks;
-      if (on) {
-        widen8(rx[c], v[c]);
-        if (r) {
-          float u[8];
-          widen8(rr[c], u);
+      widen8(rx[c], v[c]);
+      if (r) {
+        float u[8];
+        widen8(rr[c], u);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[c][i] += u[i];
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[c][i] = 0.f;
+        for (int i = 0; i < 8; ++i) v[c][i] += u[i];
       }
+      if (t + c * stride < chunks) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(v[c][i], v[c][i], ss);
+        for (int i = 0; i < 8; ++i) ss = fmaf(v[c][i], v[c][i], ss);
+      }
     }
+    load(row + step);
     ss = warp_sum(ss);
-    if constexpr (WPR > 1) {
+    if (wpr > 1) {
       // Two sets of partial sums in turn, so one barrier per pass is enough.
       if (lane == 0) part[turn][warp] = ss;
       __syncthreads();
       ss = 0.f;
-#pragma unroll
-      for (int i = 0; i < WPR; ++i) ss += part[turn][sub * WPR + i];
+      for (int i = 0; i < wpr; ++i) ss += part[turn][sub * wpr + i];
     }
     const float scale = 1.0f / sqrtf(ss * inv + p.eps);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int k = t + c * 32 * WPR;
+      const int k = t + c * stride;
       const bool on = live && k < chunks;
       if (on && p.sum.data) store8(static_cast<T *>(p.sum.data) + row * p.sum.ld + 8 * k, v[c]);
+      float w[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[c][i] = v[c][i] * scale * w[c][i];
+      for (int i = 0; i < 8; ++i) w[i] = 1.0f;
+      if (p.weight && on) {
+        const float4 a = __ldg(reinterpret_cast<const float4 *>(p.weight) + 2 * k);
+        const float4 b = __ldg(reinterpret_cast<const float4 *>(p.weight) + 2 * k + 1);
+        w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+        w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[c][i] = v[c][i] * scale * w[i];
       if constexpr (OUT8) {
         float m = amax8(v[c]);
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
@@ -309,13 +306,13 @@ bool aligned(const void *p, int64_t ld, int64_t elt) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (ld * elt) % 16 == 0;
 }
 
-// Blocks that the device holds at once: a grid of that size walks the rows with
-// the weight in registers and no second wave. Asked once per kernel and device.
+// Blocks that the device holds at once: a grid of that size walks the rows with no
+// second wave. Asked once per kernel, block size and device.
 template <typename K>
-cudaError_t resident_blocks(K kernel, std::atomic<int> (&known)[64], const DeviceFacts &dev, int64_t *blocks) {
+cudaError_t resident_blocks(K kernel, int threads, std::atomic<int> (&known)[64], const DeviceFacts &dev, int64_t *blocks) {
   int per_sm = dev.device < 64 ? known[dev.device].load(std::memory_order_relaxed) : 0;
   if (per_sm == 0) {
-    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kNormThreads, 0);
+    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, 0);
     if (e != cudaSuccess) return e;
     if (per_sm < 1) per_sm = 1;
     if (dev.device < 64) known[dev.device].store(per_sm, std::memory_order_relaxed);
@@ -324,15 +321,16 @@ cudaError_t resident_blocks(K kernel, std::atomic<int> (&known)[64], const Devic
   return cudaSuccess;
 }
 
-template <typename T, bool OUT8, int WPR, int CH>
-cudaError_t run_norm(const NormParams &p, const DeviceFacts &dev, cudaStream_t st) {
-  constexpr int kRows = kNormThreads / 32 / WPR;
-  static std::atomic<int> known[64];
+template <typename T, bool OUT8, int CH>
+cudaError_t run_norm(const NormParams &p, int wpr, const DeviceFacts &dev, cudaStream_t st) {
+  static std::atomic<int> known[9][64];
+  const int rows = kNormThreads / 32 / wpr;        // per block and pass, >= 1
+  const int threads = rows * wpr * 32;
   int64_t grid = 0;
-  const cudaError_t e = resident_blocks(norm_kernel<T, OUT8, WPR, CH>, known, dev, &grid);
+  const cudaError_t e = resident_blocks(norm_kernel<T, OUT8, CH>, threads, known[wpr], dev, &grid);
   if (e != cudaSuccess) return e;
-  const int64_t need = (p.rows + kRows - 1) / kRows;
-  norm_kernel<T, OUT8, WPR, CH><<<static_cast<unsigned>(need < grid ? need : grid), kNormThreads, 0, st>>>(p);
+  const int64_t need = (static_cast<int64_t>(p.rows) + rows - 1) / rows;
+  norm_kernel<T, OUT8, CH><<<static_cast<unsigned>(need < grid ? need : grid), threads, 0, st>>>(p, wpr);
   return cudaGetLastError();
 }
 
@@ -352,19 +350,23 @@ cudaError_t pick_norm(const NormParams &p, cudaStream_t st) {
     norm_any_kernel<T, OUT8><<<static_cast<unsigned>(p.rows < grid ? p.rows : grid), kNormThreads, 0, st>>>(p);
     return cudaGetLastError();
   }
-  // Fewest warps per row that keep it at three chunks a lane (24 fp32 values,
-  // as many weights, and the raw loads in flight).
-  const int per_warp = (p.cols + 255) / 256;         // chunks per lane with one warp
-  if (per_warp <= 1) return run_norm<T, OUT8, 1, 1>(p, dev, st);
-  if (per_warp <= 2) return run_norm<T, OUT8, 1, 2>(p, dev, st);
-  if (per_warp <= 3) return run_norm<T, OUT8, 1, 3>(p, dev, st);
-  if (per_warp <= 4) return run_norm<T, OUT8, 2, 2>(p, dev, st);
-  if (per_warp <= 6) return run_norm<T, OUT8, 2, 3>(p, dev, st);
-  if (per_warp <= 8) return run_norm<T, OUT8, 4, 2>(p, dev, st);
-  if (per_warp <= 12) return run_norm<T, OUT8, 4, 3>(p, dev, st);
-  if (per_warp <= 16) return run_norm<T, OUT8, 8, 2>(p, dev, st);
-  if (per_warp <= 24) return run_norm<T, OUT8, 8, 3>(p, dev, st);
-  return run_norm<T, OUT8, 8, 4>(p, dev, st);
+  // Warps per row and chunks per lane that leave the fewest lanes idle; among
+  // those the most chunks, for more bytes in flight per lane.
+  const int chunks = p.cols / 8;
+  int wpr = 8, ch = 4;
+  for (int c = 4; c >= 1; --c) {
+    const int w = (chunks + 32 * c - 1) / (32 * c);
+    if (w <= 8 && w * c < wpr * ch) {
+      wpr = w;
+      ch = c;
+    }
+  }
+  switch (ch) {
+    case 1: return run_norm<T, OUT8, 1>(p, wpr, dev, st);
+    case 2: return run_norm<T, OUT8, 2>(p, wpr, dev, st);
+    case 3: return run_norm<T, OUT8, 3>(p, wpr, dev, st);
+    default: return run_norm<T, OUT8, 4>(p, wpr, dev, st);
+  }
 }
 
 unsigned convert_grid(const ConvertParams &p, int sms) {
