@@ -13,9 +13,8 @@
 //   E4M3 output: a block of 32 columns is four neighbouring lanes' chunks, so its
 //   largest magnitude takes two shuffles; the codes are made from the fp32
 //   values, not from their bf16 rounding.
-//   Rows that 16-byte loads cannot take (odd widths or strides) or that
-//   registers cannot hold (over 8192 columns) go through a block per row that
-//   reads the row twice (the second time mostly from L1/L2).
+//   Rows that 16-byte loads cannot take (odd widths or strides) or that are too
+//   wide (over 8192 columns) go through a block per row, element by element.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -185,11 +184,16 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormParams p, 
   }
 }
 
-// Any width, alignment and stride: one block per row, the row read twice. A
-// thread's elements are the same in both readings, so outputs may be the inputs.
-template <typename T, bool OUT8>
-__global__ void __launch_bounds__(kNormThreads) norm_any_kernel(const NormParams p) {
-  __shared__ float part[2][kNormThreads / 32];
+// Any width, alignment and stride: one block per row, element by element. Up to
+// 2048 columns the row stays in registers (KEEP), all its loads in flight at once;
+// longer rows are read twice. A thread's elements are the same in both readings,
+// so outputs may be the inputs.
+constexpr int kAnyThreads = 128;
+constexpr int kAnyKeep = 16;
+
+template <typename T, bool OUT8, bool KEEP>
+__global__ void __launch_bounds__(kAnyThreads) norm_any_kernel(const NormParams p) {
+  __shared__ float part[2][kAnyThreads / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float inv = 1.0f / static_cast<float>(p.cols);
   const int block_tiles = (p.cols + 127) >> 7;
@@ -197,21 +201,43 @@ __global__ void __launch_bounds__(kNormThreads) norm_any_kernel(const NormParams
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
     const T *x = static_cast<const T *>(p.x.data) + row * p.x.ld;
     const T *r = p.residual.data ? static_cast<const T *>(p.residual.data) + row * p.residual.ld : nullptr;
+    float held[KEEP ? kAnyKeep : 1];
     float ss = 0.f;
-    for (int64_t k = threadIdx.x; k < p.cols; k += kNormThreads) {
-      const float v = widen(x[k]) + (r ? widen(r[k]) : 0.f);
-      ss = fmaf(v, v, ss);
+    if constexpr (KEEP) {
+      T a[kAnyKeep], b[kAnyKeep];
+#pragma unroll
+      for (int j = 0; j < kAnyKeep; ++j) {
+        const int k = threadIdx.x + j * kAnyThreads;
+        if (k < p.cols) a[j] = x[k];
+      }
+      if (r) {
+#pragma unroll
+        for (int j = 0; j < kAnyKeep; ++j) {
+          const int k = threadIdx.x + j * kAnyThreads;
+          if (k < p.cols) b[j] = r[k];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kAnyKeep; ++j) {
+        const bool on = threadIdx.x + j * kAnyThreads < static_cast<unsigned>(p.cols);
+        held[j] = on ? widen(a[j]) + (r ? widen(b[j]) : 0.f) : 0.f;
+        ss = fmaf(held[j], held[j], ss);
+      }
+    } else {
+      for (int64_t k = threadIdx.x; k < p.cols; k += kAnyThreads) {
+        const float v = widen(x[k]) + (r ? widen(r[k]) : 0.f);
+        ss = fmaf(v, v, ss);
+      }
     }
     ss = warp_sum(ss);
     if (lane == 0) part[turn][warp] = ss;
     __syncthreads();
     ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < kNormThreads / 32; ++i) ss += part[turn][i];
+    for (int i = 0; i < kAnyThreads / 32; ++i) ss += part[turn][i];
     const float scale = 1.0f / sqrtf(ss * inv + p.eps);
     // cols is a multiple of 32 for E4M3, so a warp is wholly in or out there.
-    for (int64_t k = threadIdx.x; k < p.cols; k += kNormThreads) {
-      const float s = widen(x[k]) + (r ? widen(r[k]) : 0.f);
+    auto finish = [&](int64_t k, float s) {
       const float v = s * scale * (p.weight ? __ldg(p.weight + k) : 1.0f);
       if (p.sum.data) narrow(static_cast<T *>(p.sum.data) + row * p.sum.ld + k, s);
       if constexpr (OUT8) {
@@ -225,6 +251,16 @@ __global__ void __launch_bounds__(kNormThreads) norm_any_kernel(const NormParams
       } else {
         narrow(static_cast<T *>(p.out.data) + row * p.out.ld + k, v);
       }
+    };
+    if constexpr (KEEP) {
+#pragma unroll
+      for (int j = 0; j < kAnyKeep; ++j) {
+        const int k = threadIdx.x + j * kAnyThreads;
+        if (k < p.cols) finish(k, held[j]);
+      }
+    } else {
+      for (int64_t k = threadIdx.x; k < p.cols; k += kAnyThreads)
+        finish(k, widen(x[k]) + (r ? widen(r[k]) : 0.f));
     }
   }
 }
@@ -346,8 +382,10 @@ cudaError_t pick_norm(const NormParams &p, cudaStream_t st) {
                    aligned(p.out.data, p.out.ld, OUT8 ? 1 : elt) &&
                    (reinterpret_cast<uintptr_t>(p.weight) & 15u) == 0;
   if (!vec) {
-    const int64_t grid = static_cast<int64_t>(dev.sms) * 8;
-    norm_any_kernel<T, OUT8><<<static_cast<unsigned>(p.rows < grid ? p.rows : grid), kNormThreads, 0, st>>>(p);
+    const int64_t most = static_cast<int64_t>(dev.sms) * 16;
+    const unsigned grid = static_cast<unsigned>(p.rows < most ? p.rows : most);
+    if (p.cols <= kAnyThreads * kAnyKeep) norm_any_kernel<T, OUT8, true><<<grid, kAnyThreads, 0, st>>>(p);
+    else norm_any_kernel<T, OUT8, false><<<grid, kAnyThreads, 0, st>>>(p);
     return cudaGetLastError();
   }
   // Warps per row and chunks per lane that leave the fewest lanes idle; among
