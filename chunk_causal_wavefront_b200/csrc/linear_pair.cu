@@ -246,35 +246,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MX, BN>::kThre
     const int res_bar = S::kRes0 + warp * kBufs;
     uint32_t res_phase = 0;                              // bit per buffer
     uint32_t res_pending = 0;                            // lane 0: boxes in flight
-    // First row and column of a step of a tile; false: wholly outside out.
-    auto place = [&](int t, int c, int &row0, int &col0) {
-      int mt, nt;
-      decode(g, t, mt, nt);
-      row0 = mt * 256 + static_cast<int>(rank) * 128 + wr;
-      col0 = nt * BN + e * S::kCols + c * 32;
-      return row0 < p.M && col0 < p.N;
+    // This warp's first row and column of a tile; past the last tile: outside out.
+    auto place = [&](int t, int &row, int &col) {
+      int mt = 0, nt = 0;
+      if (t < g.total) decode(g, t, mt, nt);
+      row = t < g.total ? mt * 256 + static_cast<int>(rank) * 128 + wr : p.M;
+      col = nt * BN + e * S::kCols;
     };
-    auto fetch = [&](int t, int c, int buf) {            // lane 0: residual box of a step
-      int row0, col0;
-      if (t < g.total && place(t, c, row0, col0)) {
+    auto fetch = [&](int row, int col, int buf) {        // lane 0: residual box of a step
+      if (row < p.M && col < p.N) {
         res_pending |= 1u << buf;
         mbar_arrive_expect_tx(bars + res_bar + buf, kBufBytes);
-        tma_load_2d(bufs + buf * kBufBytes, &tr, bars + res_bar + buf, col0, row0);
+        tma_load_2d(bufs + buf * kBufBytes, &tr, bars + res_bar + buf, col, row);
       }
     };
-    auto bias_at = [&](int t, int c) {                   // this lane's column of a step
-      int row0, col0;
-      if (!p.bias || t >= g.total) return 0.f;
-      place(t, c, row0, col0);
-      return col0 + lane < p.N ? __ldg(p.bias + col0 + lane) : 0.f;
+    auto bias_at = [&](int col) {                        // this lane's column of a step
+      return p.bias && col + lane < p.N ? __ldg(p.bias + col + lane) : 0.f;
     };
     int buf = 0;
-    if (g.has_residual && lane == 0) fetch(pair, 0, 0);
-    float bias = bias_at(pair, 0);
+    int row0, tile_col, row1, tile_col1;                 // this tile's and the next one's place
+    place(pair, row1, tile_col1);
+    if (g.has_residual && lane == 0) fetch(row1, tile_col1, 0);
+    float bias = bias_at(tile_col1);
     bool ok = true;
     int i = 0;
     for (int t = pair; ok && t < g.total; t += npairs, ++i) {
       const int b = i & 1;
+      row0 = row1;
+      tile_col = tile_col1;
+      place(t + npairs, row1, tile_col1);
       ok = __all_sync(0xffffffffu, wait_bar_cluster(ctx, S::kAccFull0 + b, (i >> 1) & 1));
       if (!ok) break;
       tc_fence_after();
@@ -286,18 +286,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MX, BN>::kThre
 #pragma unroll
       for (int c = 0; c < kSteps; ++c) {
         if (c + 1 < kSteps) tmem_ld32(tcol + (c + 1) * 32, nxt);
-        int row0, col0;
-        const bool on = place(t, c, row0, col0);
-        const int t1 = c + 1 < kSteps ? t : t + npairs, c1 = c + 1 < kSteps ? c + 1 : 0;
+        const int col0 = tile_col + c * 32;
+        const bool on = row0 < p.M && col0 < p.N;
+        const bool same = c + 1 < kSteps;                // the next step is of this tile
+        const int next_row = same ? row0 : row1, next_col = same ? col0 + 32 : tile_col1;
         const int buf1 = buf + 1 == kBufs ? 0 : buf + 1;
         // Of this warp's stores at most the last one may still be reading its
         // buffer: buf (three steps ago) and buf1 (two steps ago) are free.
         if (lane == 0) {
           asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-          if (g.has_residual) fetch(t1, c1, buf1);
+          if (g.has_residual) fetch(next_row, next_col, buf1);
         }
         bias_row[lane] = bias;
-        bias = bias_at(t1, c1);
+        bias = bias_at(next_col);
         __syncwarp();
         if (on) {
           float v[32];
@@ -381,7 +382,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MX, BN>::kThre
           // One store for both steps; columns past N are clipped.
           if (c + 1 == kSteps) {
             if (lane == 0) {
-              if (place(t, 0, row0, col0)) tma_store_2d(&to, bufs + buf * kBufBytes, col0, row0);
+              if (row0 < p.M && tile_col < p.N) tma_store_2d(&to, bufs + buf * kBufBytes, tile_col, row0);
               tma_store_commit();
             }
             buf = buf1;
@@ -403,7 +404,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MX, BN>::kThre
           // Last TMEM load of this accumulator done: release it to the leader.
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(bars + S::kAccEmpty0 + b, 0);
+          if (lane == 0) mbar_arrive_cluster_relaxed(bars + S::kAccEmpty0 + b, 0);
         }
       }
     }

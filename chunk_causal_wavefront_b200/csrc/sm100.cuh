@@ -588,5 +588,18 @@ __device__ __forceinline__ void store_cluster_f32(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
+// Arrive on CTA `cta`'s copy of a local mbarrier without publishing memory: for a
+// phase that says only that tcgen05.ld results have arrived in registers. (The
+// releasing form waits for the thread's earlier stores, about 2000 cycles behind
+// global ones.)
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(const uint64_t *bar, uint32_t cta) {
+  asm volatile(
+      "{\n\t.reg .b32 ra;\n\t"
+      "mapa.shared::cluster.u32 ra, %0, %1;\n\t"
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [ra];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(cta)
+      : "memory");
+}
+
 }  // namespace sm100
 }  // namespace wf
