@@ -27,8 +27,8 @@ _TYPES = {torch.bfloat16: _wf.WF_DTYPE_BF16, torch.float32: _wf.WF_DTYPE_F32}
 _ACTS = {"none": _wf.WF_ACT_NONE, "gelu": _wf.WF_ACT_GELU, "silu": _wf.WF_ACT_SILU}
 
 
-_NO_GRAD = "row operators compute no gradients: call them under torch.no_grad()"
-# The current stream's handle without a Stream object around it.
+# The current device, and its current stream's handle, without the objects around them.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
@@ -71,6 +71,11 @@ class E4M3Rows:
     @property
     def device(self) -> torch.device:
         return self.codes.device
+
+    requires_grad = False
+
+    def get_device(self) -> int:
+        return self.codes.get_device()
 
     def first(self, rows: int) -> "E4M3Rows":
         """The first rows, sharing memory."""
@@ -149,24 +154,20 @@ def _check(status: int, what: str) -> None:
 def _here(stream, x, *others) -> Optional[int]:
     """Checks that everything is on one CUDA device. The raw current stream if that device is
     current and no stream is given; else None: the call goes through _elsewhere."""
-    device = x.device
-    if device.type != "cuda":
+    index = x.get_device()
+    if index < 0:
         raise ValueError("row operators need CUDA tensors")
-    grad = torch.is_grad_enabled()
-    if grad and type(x) is not E4M3Rows and x.requires_grad:
-        raise ValueError(_NO_GRAD)
     for t in others:
-        if t is not None:
-            if t.device != device:
-                raise ValueError(f"all tensors must be on one device: got {device} and {t.device}")
-            if grad and type(t) is not E4M3Rows and t.requires_grad:
-                raise ValueError(_NO_GRAD)
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"all tensors must be on one device: got {x.device} and {t.device}")
+    if torch.is_grad_enabled() and (x.requires_grad or any([t is not None and t.requires_grad
+                                                            for t in others])):
+        raise ValueError("row operators compute no gradients: call them under torch.no_grad()")
     if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+        if stream.device != x.device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {x.device}")
         return None
-    index = device.index
-    return _raw_stream(index) if index == torch.cuda.current_device() else None
+    return _raw_stream(index) if index == _current_device() else None
 
 
 @contextlib.contextmanager
@@ -200,7 +201,7 @@ def _given(out: Operand, shape, out_dtype) -> Operand:
 def _new(like: torch.Tensor, shape, out_dtype, default: torch.dtype) -> Operand:
     """A new output on the device of `like`."""
     if out_dtype is None or out_dtype is default:
-        return like.new_empty(shape, dtype=default)
+        return like.new_empty(shape) if like.dtype is default else like.new_empty(shape, dtype=default)
     if out_dtype == "e4m3":
         rows, cols = math.prod(shape[:-1]), shape[-1]
         if cols % 32:
@@ -210,6 +211,10 @@ def _new(like: torch.Tensor, shape, out_dtype, default: torch.dtype) -> Operand:
         out.scales = like.new_empty((rows + 127) // 128 * ((cols + 127) // 128) * 512, dtype=torch.uint8)
         return out
     raise ValueError(f"out_dtype must be {default} (the default) or 'e4m3'")
+
+
+def _packed_like(x: torch.Tensor) -> torch.Tensor:
+    return x.new_empty(x.shape)
 
 
 def quantize_rows(x: torch.Tensor, out: Optional[E4M3Rows] = None, stream=None) -> E4M3Rows:
@@ -248,12 +253,21 @@ def add_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *,
                                 out_dtype=out_dtype)
     xr = _rows(x)
     w = None if weight is None else _vector(weight, shape[-1], "weight")
-    out = _new(x, shape, out_dtype, x.dtype) if out is None else _given(out, shape, out_dtype)
+    if x.is_contiguous():                     # new rows have x's layout
+        new = torch.empty_like
+    else:
+        new = _packed_like
+    if out is not None:
+        _given(out, shape, out_dtype)
+    elif out_dtype is None or out_dtype is x.dtype:
+        out = new(x)
+    else:
+        out = _new(x, shape, out_dtype, x.dtype)
     if residual is None:
         _check(_norm(xr, None, w, eps, None, _rows(out), raw), "wf_add_rms_norm")
         return out
     if sum_out is None:
-        sum_out = x.new_empty(shape)
+        sum_out = new(x)
     _check(_norm(xr, _rows(residual), w, eps, _rows(sum_out), _rows(out), raw), "wf_add_rms_norm")
     return out, sum_out
 
