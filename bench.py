@@ -56,6 +56,10 @@ def parse():
     ap.add_argument("--kv", choices=["bf16", "fp8"], default="bf16",
                     help="pool storage: bf16, or E4M3 codes with block scales and FP8 "
                          "tensor-core attention")
+    ap.add_argument("--layer", choices=["bf16", "e4m3"], default=None,
+                    help="step = one whole transformer layer on the round (norms, projections, "
+                         "attention, feed-forward of 4 x hidden) with dummy weights in this type, "
+                         "+ advance; --kv picks the pool")
     ap.add_argument("--mask", choices=["wf", "rf"], default="wf",
                     help="wf: M_WF chunk-causal mask; rf: bidirectional live window")
     ap.add_argument("--e2e-steps", type=int, default=30)
@@ -475,6 +479,86 @@ def run_ours(args, ws, rank, local):
     return res
 
 
+def run_layer(args, ws, rank, local):
+    """Whole layers on steady rounds (LayerRound.run + wf_advance_round), device-timed."""
+    import torch
+    import torch.distributed as dist
+    import wf_inputs
+    from chunk_causal_wavefront_b200 import KVPool, LayerRound, LayerWeights, make_config, rows_check_status
+
+    cfg = wf_inputs.CONFIGS[args.config].replace(mask=args.mask)
+    dev = torch.device("cuda", local)
+    torch.cuda.set_device(dev)
+    steady = cfg.steady_round()
+    npages = (cfg.num_stages + 1 + cfg.anchor_chunks + cfg.history_chunks) * cfg.pages_per_chunk
+    pool = KVPool(make_config(num_stages=cfg.num_stages, chunk_tokens=cfg.chunk_tokens,
+                              num_heads=cfg.num_heads, head_dim=cfg.head_dim,
+                              anchor_chunks=cfg.anchor_chunks, history_chunks=cfg.history_chunks,
+                              page_tokens=cfg.page_tokens, num_layers=1,
+                              dtype="fp8" if args.kv == "fp8" else cfg.dtype, rope=cfg.rope,
+                              frames_per_chunk=cfg.frames_per_chunk, grid_h=cfg.grid_h,
+                              grid_w=cfg.grid_w, rope_split=cfg.rope_split, rope_base=cfg.rope_base,
+                              max_rounds=steady + args.warmup + args.steps + 4, mask=cfg.mask),
+                  device=dev, page_order=wf_inputs.draw_page_order(npages, cfg.seed + 1))
+    hidden = cfg.num_heads * cfg.head_dim
+    ffn = 4 * hidden
+    gen = torch.Generator(device=dev).manual_seed(cfg.seed * 1000 + rank)
+    m = lambda n, k: (torch.randn(n, k, generator=gen, device=dev) / math.sqrt(k)).bfloat16()
+    weights = LayerWeights(w_qkv=m(3 * hidden, hidden), w_out=m(hidden, hidden), w_up=m(ffn, hidden),
+                           w_down=m(hidden, ffn), b_out=torch.zeros(hidden, device=dev),
+                           b_up=torch.zeros(ffn, device=dev), b_down=torch.zeros(hidden, device=dev))
+    if args.layer == "e4m3":
+        weights = weights.to_e4m3()
+    layer = LayerRound(pool, ffn)
+    # Two streams in turn; the pre-norms keep their growth from mattering to the arithmetic.
+    h = [torch.randn(cfg.num_slots, cfg.chunk_tokens, hidden, generator=gen, device=dev).bfloat16()
+         for _ in range(2)]
+
+    def step(i):
+        layer.run(0, h[i & 1], weights)
+        pool.advance()
+
+    for i in range(steady + args.warmup):
+        step(i)
+    layout = pool.layout()
+    rows = pool.live_rows
+    flops = unmasked_flops(layout, cfg) + 2 * rows * (4 * hidden * hidden + 2 * hidden * ffn)
+    a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    clocks = ClockSampler(local)
+    if ws > 1:
+        dist.barrier()
+    torch.cuda.synchronize()
+    clocks.start()
+    time.sleep(0.3)
+    a.record()
+    for i in range(args.steps):
+        step(i)
+    b.record()
+    torch.cuda.synchronize()
+    clk = clocks.stop()
+    if ws > 1:
+        dist.barrier()
+    for st in (pool.check_status(), rows_check_status(dev)):
+        if st != 0:
+            raise RuntimeError(f"device status {st} after timed steps")
+    ms, = max_over_ranks([a.elapsed_time(b)], dev)
+    pool.close()
+    separate = args.layer == "e4m3" or args.kv == "fp8"    # q, k, v products, then publication
+    launches = 8 + (3 if separate else 0) + (1 if args.layer == "e4m3" else 0)
+    return {"metric": "WF layer-round TFLOP/s (unmasked attention and products)",
+            "value": whole_job_rate(flops * args.steps, ms, ws) / 1e12, "unit": UNIT, "n_gpus": ws,
+            "steps": args.steps, "warmup": args.warmup, "ms_per_step": ms / args.steps,
+            "higher_is_better": True, "scaling": "weak", "vs_baseline": None, "dtype": args.layer,
+            "data": "synthetic",
+            "config": {"workload": f"{cfg.name}: one whole layer on a steady round, hidden {hidden}, "
+                                   f"ffn {ffn}, {args.layer} products, {args.kv} pool, {rows} rows",
+                       "step": "LayerRound.run + wf_advance_round",
+                       "l2": "working set > 126 MB L2; no flush",
+                       "parallelism": f"replicas x{ws}" if ws > 1 else "single GPU"},
+            "flops_per_step": flops, "layer_rounds_per_s": ws * args.steps / (ms * 1e-3),
+            "clocks": clk, "gpu_launches": launches * args.steps}
+
+
 # ------------------------------------------------------------------- oracle timing
 
 ORACLE_SAMPLE_ROWS = 64
@@ -706,6 +790,8 @@ def main():
     args = parse()
     if args.fused and args.kv == "fp8":
         raise SystemExit("--fused publishes into bf16 pools only")
+    if args.layer and (args.fused or args.config not in ("wan13b_bf16", "wan13b_5step_bf16", "wan14b_bf16")):
+        raise SystemExit("--layer runs on the single-layer bf16 configurations, without --fused")
     if args.gpus > 1 and "WORLD_SIZE" not in os.environ:
         # one process per GPU: relaunch as args.gpus ranks
         sys.exit(spawn_ranks(args.gpus, sys.argv[1:]))
@@ -753,6 +839,15 @@ def main():
                 "clocks": res["clocks"],
                 "gpu_launches": res["rounds"] * (2 * res["layers"] + 1),
             }
+            print(json.dumps(line), flush=True)
+        if ws > 1:
+            import torch.distributed as dist
+            dist.barrier()
+            dist.destroy_process_group()
+        return
+    if args.layer:
+        line = run_layer(args, ws, rank, local)
+        if rank == 0:
             print(json.dumps(line), flush=True)
         if ws > 1:
             import torch.distributed as dist

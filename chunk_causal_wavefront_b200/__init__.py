@@ -14,10 +14,11 @@ from .wf import (LIB_PATH, WF_ACT_GELU, WF_ACT_NONE, WF_ACT_SILU, WF_DTYPE_BF16,
                  WF_ROPE_OFF, WfError,
                  WfPoolConfig, wf_status_string)
 from .pool import KVPool, make_config
+from .layer import LayerRound, LayerWeights
 from .rows import (E4M3Rows, add_rms_norm, linear, quantize_rows, rows_check_status)
 
 __all__ = [
-    "KVPool", "make_config", "E4M3Rows", "add_rms_norm", "linear", "quantize_rows",
+    "KVPool", "make_config", "LayerRound", "LayerWeights", "E4M3Rows", "add_rms_norm", "linear", "quantize_rows",
     "rows_check_status", "WF_ACT_NONE", "WF_ACT_GELU", "WF_ACT_SILU", "WfError", "WfPoolConfig", "wf_status_string", "LIB_PATH",
     "WF_OK", "WF_ERR_INVALID_ARG", "WF_ERR_OUT_OF_PAGES", "WF_ERR_NOT_READY", "WF_ERR_BAD_PAGE",
     "WF_ERR_CALL_ORDER", "WF_ERR_CUDA", "WF_ERR_UNSUPPORTED", "WF_ERR_TIMEOUT",

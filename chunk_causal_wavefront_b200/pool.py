@@ -164,6 +164,13 @@ class KVPool:
         g = self.geometry
         return _wf.wf_pool_get_layout(self.handle, g.max_positions, g.pages_per_chunk)
 
+    @property
+    def live_rows(self) -> int:
+        """Token rows of the round's live slots: the first rows of [S+1][C][...] buffers (the
+        store, the last slot, is live only when every other slot is)."""
+        k, stages = self.round, self.cfg.num_stages
+        return (min(k + 1, stages) + (k >= stages)) * self.cfg.chunk_tokens
+
     def pages_view(self) -> torch.Tensor:
         """The page region as [layers][num_pages][2][heads][P][d] (K = 0, V = 1)."""
         g, c = self.geometry, self.cfg

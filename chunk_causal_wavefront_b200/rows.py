@@ -81,6 +81,13 @@ class E4M3Rows:
         """The first rows, sharing memory."""
         return E4M3Rows(self.codes[:rows], self.scales)
 
+    def span(self, start: int, stop: int) -> "E4M3Rows":
+        """Rows [start, stop), sharing memory; start is a multiple of 128 (the scales' tiles)."""
+        rows, cols = self.codes.shape
+        if start % 128 or not 0 <= start <= stop <= rows:
+            raise ValueError("a span of E4M3 rows starts at a multiple of 128 inside them")
+        return E4M3Rows(self.codes[start:stop], self.scales[start // 128 * ((cols + 127) // 128) * 512:])
+
     def dequantize(self, out: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.bfloat16,
                    stream=None) -> torch.Tensor:
         """The values these rows stand for, as bf16 or fp32 (exact in both)."""

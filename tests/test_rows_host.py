@@ -199,10 +199,32 @@ def test_row_descriptions():
             PR._rows(bad)
 
 
+def test_live_rows_and_layer_refusals():
+    def pool(dtype="bf16"):
+        return wfb.KVPool(wfb.make_config(num_stages=2, chunk_tokens=128, num_heads=2, head_dim=128,
+                                          anchor_chunks=1, history_chunks=1, page_tokens=128, dtype=dtype))
+    p = pool()
+    seen = []
+    for _ in range(4):
+        live = [r[2] for r in p.layout() if r[2] is not None]
+        assert sorted(live) == list(range(len(live)))          # a prefix of the slots
+        assert p.live_rows == 128 * len(live)
+        seen.append(p.live_rows)
+        p.advance()
+    assert seen == [128, 256, 384, 384]
+    with pytest.raises(ValueError, match="bf16 and FP8"):
+        wfb.LayerRound(pool("f32"), 256)
+
+
 def test_e4m3_rows_checks():
     codes = torch.zeros(130, 96, dtype=torch.float8_e4m3fn)
     q = wfb.E4M3Rows(codes, torch.zeros(1024, dtype=torch.uint8))
     assert q.first(3).shape == (3, 96)
+    s = q.span(128, 130)
+    assert s.shape == (2, 96) and s.scales.data_ptr() == q.scales.data_ptr() + 512
+    for start, stop in ((1, 2), (128, 131), (128, 0), (-128, 0)):
+        with pytest.raises(ValueError):
+            q.span(start, stop)
     with pytest.raises(ValueError):
         wfb.E4M3Rows(codes, torch.zeros(1023, dtype=torch.uint8))
     with pytest.raises(ValueError):
