@@ -4,14 +4,21 @@
 //
 //   out[m][n] = act(sum_k x[m][k] w[n][k] + bias[n]) + residual[m][n]
 //
-// The tensor cores bound it. Tile: 256 rows x BN features per pair of CTAs, each
-// CTA holding 128 rows of x and BN / 2 features of w per k-block of 128 bytes;
-// the leader issues M = 256, N = BN MMAs, every CTA receives the accumulator of
-// its own 128 rows in its own TMEM, and two accumulators take turns, so that one
-// tile's epilogue runs under the next tile's products.
-//   BN = 256 is for bf16 only (two accumulators fill TMEM); BN = 192 leaves 128
-//   columns, which hold four stages of scales for E4M3. The launch takes
-//   whichever wastes less of the last wave.
+// Tile: 256 rows x BN features per pair of CTAs, each CTA holding 128 rows of x and
+// BN / 2 features of w per k-block of 128 bytes; the leader issues M = 256, N = BN
+// MMAs, every CTA receives the accumulator of its own 128 rows in its own TMEM, and
+// two accumulators take turns, so that one tile's epilogue runs under the next
+// tile's products. BN = 256 is for bf16 only (two accumulators fill TMEM); BN = 192
+// leaves 128 columns, which hold four stages of scales for E4M3.
+//   What bounds it is not the tensor pipe but the operands' way from L2 (without
+// loads 4680 x 20480 x 5120 bf16 takes 501 us at 1965 MHz, with them 640, and the
+// number of stages changes nothing). So a tile may have two halves of BN = 192
+// features that share the row operand (384 wide): 29 % fewer bytes per product,
+// but each half has one accumulator. The halves' products are reordered at a
+// tile's ends to give the epilogue time; what of it stays exposed, about 3 us per
+// tile, pays only for long K: 23400 x 1536 x 6144 E4M3 206 (192) and 194 us (384)
+// under the power cap, x 1536 x 1536 bf16 100 (256), 102 (384) and 105 us (192). 512
+// wide (two halves of 256) was never the best by more than 2 %.
 // Tiles are walked in groups of 8 row tiles, feature tiles slowest inside a
 // group, so that the tiles in flight cover a near-square patch of the output and
 // both operands are re-read from L2.
@@ -48,18 +55,21 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kBufs = 3;                        // staging buffers per epilogue warp
 constexpr uint32_t kBufBytes = 32 * 64;         // 32 rows x 32 bf16 columns
 constexpr int kGroup = 8;                       // row tiles per raster group
 constexpr int kScaleCols = 384;                 // first TMEM column of the scales
 constexpr uint32_t kABytes = 128 * 128;
 
-template <bool MX, int BN>
+template <bool MX, int BN, int HALVES>
 struct Shape {
-  static constexpr uint32_t kBBytes = BN / 2 * 128;
-  static constexpr uint32_t kScaleBytes = MX ? 512 + 1024 : 0;
+  static constexpr uint32_t kHalfBytes = BN / 2 * 128;        // one half's features of w
+  static constexpr uint32_t kBBytes = HALVES * kHalfBytes;
+  // Scale tiles of 128 rows: one of x, and those that cover HALVES * BN rows of w.
+  static constexpr int kScaleTiles = MX ? (HALVES * BN + 127) / 128 : 0;
+  static constexpr uint32_t kScaleBytes = MX ? 512 + 512 * kScaleTiles : 0;
   static constexpr uint32_t kStageBytes = kABytes + kBBytes + kScaleBytes;   // per CTA
-  static constexpr int kStages = 5;
+  static constexpr int kStages = HALVES == 2 ? 4 : 5;
+  static constexpr int kBufs = HALVES == 2 ? 2 : 3;           // staging buffers per epilogue warp
   // Epilogue: warpgroups of kCols columns. Three at BN = 192 (registers allow no
   // more at 256, where the accumulator's columns are shared by two).
   static constexpr int kCols = BN == 192 ? 64 : 128;
@@ -89,6 +99,8 @@ struct Shape {
   static_assert(kOperandBytes % 1024 == 0 && kOffBuf % 512 == 0, "alignment");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
   static_assert(!MX || 2 * BN <= kScaleCols, "TMEM");
+  static_assert(HALVES == 1 || 2 * kStages <= kWideMinBlocks, "k-blocks of a wide tile");
+  static_assert(!MX || 4 * 4 * (1 + kScaleTiles) <= 512 - kScaleCols, "TMEM");
 };
 
 struct PairGrid {
@@ -105,13 +117,13 @@ __device__ __forceinline__ void decode(const PairGrid &g, int t, int &mt, int &n
   mt = grp * kGroup + (r - nt * gm);
 }
 
-template <bool MX, int BN, bool OUT8>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MX, BN>::kThreads, 1)
+template <bool MX, int BN, int HALVES, bool OUT8>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MX, BN, HALVES>::kThreads, 1)
     linear_pair_kernel(const __grid_constant__ LinearParams p, const __grid_constant__ PairGrid g,
                        const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw,
                        const __grid_constant__ CUtensorMap tsx, const __grid_constant__ CUtensorMap tsw,
                        const __grid_constant__ CUtensorMap tr, const __grid_constant__ CUtensorMap to) {
-  using S = Shape<MX, BN>;
+  using S = Shape<MX, BN, HALVES>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -148,7 +160,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MX, BN>::kThre
       int mt, nt;
       decode(g, t, mt, nt);
       const int row0 = mt * 256 + static_cast<int>(rank) * 128;
-      const int col0 = nt * BN;
+      const int col0 = nt * (HALVES * BN);
       for (int kb = 0; kb < g.n_kb; ++kb, ++q) {
         const int s = q % S::kStages;
         ok = __all_sync(0xffffffffu, wait_bar(ctx, S::kEmpty0 + s, ((q / S::kStages) & 1) ^ 1));
@@ -159,7 +171,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MX, BN>::kThre
           uint8_t *sa = smem + s * S::kOperandBytes;
           const uint32_t lb = leader_bar(bars + S::kFull0 + s);
           tma_load_2d_pair(sa, &tx, lb, kb * S::kKElems, row0);
-          tma_load_2d_pair(sa + kABytes, &tw, lb, kb * S::kKElems, col0 + static_cast<int>(rank) * (BN / 2));
+#pragma unroll
+          for (int h = 0; h < HALVES; ++h)
+            tma_load_2d_pair(sa + kABytes + h * S::kHalfBytes, &tw, lb, kb * S::kKElems,
+                             col0 + h * BN + static_cast<int>(rank) * (BN / 2));
           if constexpr (MX) {
             uint8_t *ss = smem + S::kOffScale + s * S::kScaleBytes;
             tma_load_3d_pair(ss, &tsx, lb, 0, kb, row0 >> 7);
@@ -181,54 +196,89 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MX, BN>::kThre
       const uint32_t hi = desc_hi_sw128(1024);
       const uint32_t lo0 = desc_lo_sw128(smem_u32(smem), 16);
       const uint32_t sc0 = smem_u32(smem + S::kOffScale);
-      int q = 0, i = 0;
+      int q = 0, i = 0;                     // k-blocks and accumulators done
       bool ok = true;
-      for (int t = pair; ok && t < g.total; t += npairs, ++i) {
+      uint32_t shift = 0;
+      auto acc_empty = [&](int i) {
+        ok = __all_sync(0xffffffffu, wait_bar_cluster(ctx, S::kAccEmpty0 + (i & 1), ((i >> 1) & 1) ^ 1));
+        tc_fence_after();
+        return ok;
+      };
+      auto acc_full = [&](int i) {
+        if (elect_one()) mma_commit_pair(bars + S::kAccFull0 + (i & 1));
+        __syncwarp();
+      };
+      // Halves [h0, h1) of the products of the k-block at position qq of this CTA's
+      // sequence, kb of its tile. `first`: the scales are not in TMEM yet. `last`:
+      // the stage is free after it. A half h accumulates in columns BN ((i0 + h) & 1).
+      auto block = [&](int qq, int kb, int h0, int h1, int i0, bool first, bool last) {
+        const int s = qq % S::kStages;
+        if (first) {
+          ok = __all_sync(0xffffffffu, wait_bar_cluster(ctx, S::kFull0 + s, (qq / S::kStages) & 1));
+          if (!ok) return;
+          tc_fence_after();
+        }
+        const uint32_t a_lo = lo0 + ((s * S::kOperandBytes) >> 4);
+        const uint32_t b_lo = a_lo + (kABytes >> 4);
+        const int left = g.k_steps - kb * (S::kKElems / S::kKStep);
+        if (elect_one()) {
+          const uint32_t sfa = tmem + kScaleCols + 4 * (1 + S::kScaleTiles) * (qq & 3);
+          const uint32_t sfb = sfa + 4;
+          if (MX && first) {
+            const uint32_t sc = sc0 + s * S::kScaleBytes;
+#pragma unroll
+            for (int j = 0; j <= S::kScaleTiles; ++j)
+              tmem_copy_scales_pair(sfa + 4 * j, make_desc_scale_tile(sc + 512 * j));
+          }
+#pragma unroll
+          for (int h = 0; h < HALVES; ++h) {
+            if (h < h0 || h >= h1) continue;
+            const uint32_t d = tmem + BN * ((i0 + h) & 1);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (k >= left) continue;
+              const uint32_t add = (kb > 0 || k > 0) ? 1u : 0u;
+              if constexpr (MX)
+                mma_mx_ss2_pair(d, a_lo + k * 2, b_lo + ((h * S::kHalfBytes) >> 4) + k * 2, hi,
+                                make_idesc_mx_e4m3(256, BN, k), sfa, sfb + shift + h * (BN / 32), add);
+              else
+                mma_bf16_ss2_pair(d, a_lo + k * 2, b_lo + ((h * S::kHalfBytes) >> 4) + k * 2, hi,
+                                  make_idesc_bf16(256, BN, false), add);
+            }
+          }
+          if (last) mma_commit_pair(bars + S::kEmpty0 + s);
+        }
+        __syncwarp();
+      };
+      for (int t = pair; ok && t < g.total; t += npairs) {
         int mt, nt;
         decode(g, t, mt, nt);
-        const int b = i & 1;
-        if (!__all_sync(0xffffffffu, wait_bar_cluster(ctx, S::kAccEmpty0 + b, ((i >> 1) & 1) ^ 1))) break;
-        tc_fence_after();
         // BN = 192: odd feature tiles start at row 64 of a 128-row scale tile.
-        const uint32_t shift = (nt * BN & 127) >> 5;
-        for (int kb = 0; kb < g.n_kb; ++kb, ++q) {
-          const int s = q % S::kStages;
-          if (!__all_sync(0xffffffffu, wait_bar_cluster(ctx, S::kFull0 + s, (q / S::kStages) & 1))) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t a_lo = lo0 + ((s * S::kOperandBytes) >> 4);
-          const uint32_t b_lo = a_lo + (kABytes >> 4);
-          const int left = g.k_steps - kb * (S::kKElems / S::kKStep);
-          if (elect_one()) {
-            if constexpr (MX) {
-              const uint32_t sc = sc0 + s * S::kScaleBytes;
-              const uint32_t sfa = tmem + kScaleCols + 16 * (q & 3);
-              const uint32_t sfb = sfa + 4;
-              tmem_copy_scales_pair(sfa, make_desc_scale_tile(sc));
-              tmem_copy_scales_pair(sfb, make_desc_scale_tile(sc + 512));
-              tmem_copy_scales_pair(sfb + 4, make_desc_scale_tile(sc + 1024));
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if (k < left)
-                  mma_mx_ss2_pair(tmem + BN * b, a_lo + k * 2, b_lo + k * 2, hi,
-                                  make_idesc_mx_e4m3(256, BN, k), sfa, sfb + shift,
-                                  (kb > 0 || k > 0) ? 1u : 0u);
-            } else {
-              constexpr uint32_t idesc = make_idesc_bf16(256, BN, false);
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if (k < left)
-                  mma_bf16_ss2_pair(tmem + BN * b, a_lo + k * 2, b_lo + k * 2, hi, idesc,
-                                    (kb > 0 || k > 0) ? 1u : 0u);
-            }
-            mma_commit_pair(bars + S::kEmpty0 + s);
-          }
-          __syncwarp();
+        shift = (nt * (HALVES * BN) & 127) >> 5;
+        if constexpr (HALVES == 1) {
+          if (!acc_empty(i)) break;
+          for (int kb = 0; ok && kb < g.n_kb; ++kb, ++q) block(q, kb, 0, 1, i, true, true);
+          if (ok) acc_full(i);
+          ++i;
+        } else {
+          // The first k-blocks go through half 0 while the epilogue still drains the
+          // last tile's half 1, and the last ones finish half 0 early, so that
+          // its epilogue runs under their products of half 1.
+          // (The launch sees to n_kb >= 2 kStages.)
+          const int head = S::kStages, tail = g.n_kb - S::kStages;
+          if (!acc_empty(i)) break;
+          for (int kb = 0; ok && kb < head; ++kb) block(q + kb, kb, 0, 1, i, true, false);
+          if (!ok || !acc_empty(i + 1)) break;
+          for (int kb = 0; kb < head; ++kb) block(q + kb, kb, 1, 2, i, false, true);
+          for (int kb = head; ok && kb < tail; ++kb) block(q + kb, kb, 0, 2, i, true, true);
+          for (int kb = tail; ok && kb < g.n_kb; ++kb) block(q + kb, kb, 0, 1, i, true, false);
+          if (!ok) break;
+          acc_full(i);
+          for (int kb = tail; kb < g.n_kb; ++kb) block(q + kb, kb, 1, 2, i, false, true);
+          acc_full(i + 1);
+          q += g.n_kb;
+          i += 2;
         }
-        if (ok && elect_one()) mma_commit_pair(bars + S::kAccFull0 + b);
-        __syncwarp();
       }
       // Drain: all MMAs issued by this thread complete before TMEM is freed.
       if (elect_one()) mma_commit_pair(bars + S::kDrain);
@@ -241,17 +291,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MX, BN>::kThre
     const int e = warp >> 2;                             // warpgroup: kCols columns of the tile
     const int wr = (warp & 3) * 32;                      // first row of this warp
     const uint32_t lane_addr = static_cast<uint32_t>(wr) << 16;
-    uint8_t *bufs = smem + S::kOffBuf + warp * kBufs * kBufBytes;
+    uint8_t *bufs = smem + S::kOffBuf + warp * S::kBufs * kBufBytes;
     float *bias_row = reinterpret_cast<float *>(smem + S::kOffBias) + warp * 32;
-    const int res_bar = S::kRes0 + warp * kBufs;
+    const int res_bar = S::kRes0 + warp * S::kBufs;
     uint32_t res_phase = 0;                              // bit per buffer
     uint32_t res_pending = 0;                            // lane 0: boxes in flight
-    // This warp's first row and column of a tile; past the last tile: outside out.
-    auto place = [&](int t, int &row, int &col) {
+    // This warp's first row and column; past the last tile: outside out.
+    auto place = [&](int i, int &row, int &col) {        // of the i-th accumulator
+      const int64_t t = pair + static_cast<int64_t>(i / HALVES) * npairs;
       int mt = 0, nt = 0;
-      if (t < g.total) decode(g, t, mt, nt);
+      if (t < g.total) decode(g, static_cast<int>(t), mt, nt);
       row = t < g.total ? mt * 256 + static_cast<int>(rank) * 128 + wr : p.M;
-      col = nt * BN + e * S::kCols;
+      col = (nt * HALVES + i % HALVES) * BN + e * S::kCols;
     };
     auto fetch = [&](int row, int col, int buf) {        // lane 0: residual box of a step
       if (row < p.M && col < p.N) {
@@ -265,16 +316,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MX, BN>::kThre
     };
     int buf = 0;
     int row0, tile_col, row1, tile_col1;                 // this tile's and the next one's place
-    place(pair, row1, tile_col1);
+    place(0, row1, tile_col1);
     if (g.has_residual && lane == 0) fetch(row1, tile_col1, 0);
     float bias = bias_at(tile_col1);
     bool ok = true;
-    int i = 0;
-    for (int t = pair; ok && t < g.total; t += npairs, ++i) {
+    const int tiles = (g.total - pair + npairs - 1) / npairs;
+    for (int i = 0; ok && i < HALVES * tiles; ++i) {
       const int b = i & 1;
       row0 = row1;
       tile_col = tile_col1;
-      place(t + npairs, row1, tile_col1);
+      place(i + 1, row1, tile_col1);
       ok = __all_sync(0xffffffffu, wait_bar_cluster(ctx, S::kAccFull0 + b, (i >> 1) & 1));
       if (!ok) break;
       tc_fence_after();
@@ -290,11 +341,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MX, BN>::kThre
         const bool on = row0 < p.M && col0 < p.N;
         const bool same = c + 1 < kSteps;                // the next step is of this tile
         const int next_row = same ? row0 : row1, next_col = same ? col0 + 32 : tile_col1;
-        const int buf1 = buf + 1 == kBufs ? 0 : buf + 1;
-        // Of this warp's stores at most the last one may still be reading its
-        // buffer: buf (three steps ago) and buf1 (two steps ago) are free.
+        const int buf1 = buf + 1 == S::kBufs ? 0 : buf + 1;
+        // Stores of buf (kBufs steps ago) and buf1 (one step fewer) have been read.
         if (lane == 0) {
-          asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+          asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(S::kBufs - 2) : "memory");
           if (g.has_residual) fetch(next_row, next_col, buf1);
         }
         bias_row[lane] = bias;
@@ -410,7 +460,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MX, BN>::kThre
     }
     if (lane == 0) {
       // A fetch that no step took (another role gave up) must land before exit.
-      for (int k = 0; k < kBufs; ++k)
+      for (int k = 0; k < S::kBufs; ++k)
         if (res_pending >> k & 1) drain_wait(ctx, res_bar + k, (res_phase >> k) & 1);
       tma_store_wait_all();
     }
@@ -426,9 +476,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MX, BN>::kThre
   }
 }
 
-template <bool MX, int BN, bool OUT8>
+template <bool MX, int BN, int HALVES, bool OUT8>
 cudaError_t run_pair(const LinearParams &p, cudaStream_t st) {
-  using S = Shape<MX, BN>;
+  using S = Shape<MX, BN, HALVES>;
   const int elt = MX ? 1 : 2;
   CUtensorMap tx{}, tw{}, tsx{}, tsw{}, tr{}, to{};
   const uint64_t K = static_cast<uint64_t>(p.K), M = static_cast<uint64_t>(p.M), N = static_cast<uint64_t>(p.N);
@@ -442,7 +492,7 @@ cudaError_t run_pair(const LinearParams &p, cudaStream_t st) {
     const uint64_t kt = (K + 127) / 128;
     const uint64_t sd[3] = {128, kt, (M + 127) / 128}, qd[3] = {128, kt, (N + 127) / 128};
     const uint64_t ss[2] = {512, 512 * kt};
-    const uint32_t sb[3] = {128, 1, 1}, qb[3] = {128, 1, 2};
+    const uint32_t sb[3] = {128, 1, 1}, qb[3] = {128, 1, S::kScaleTiles};
     ok = ok && encode_rows_map(&tsx, 4, 0, p.x.scales, 3, sd, ss, sb) &&
          encode_rows_map(&tsw, 4, 0, p.w.scales, 3, qd, ss, qb);
   }
@@ -455,7 +505,7 @@ cudaError_t run_pair(const LinearParams &p, cudaStream_t st) {
   }
   if (!ok) return cudaErrorInvalidValue;
   PairGrid g{};
-  const int64_t mt = (static_cast<int64_t>(p.M) + 255) / 256, nt = (static_cast<int64_t>(p.N) + BN - 1) / BN;
+  const int64_t mt = (static_cast<int64_t>(p.M) + 255) / 256, nt = (static_cast<int64_t>(p.N) + HALVES * BN - 1) / (HALVES * BN);
   if (mt * nt > 0x7fffffff - 65536) return cudaErrorInvalidValue;
   g.m_tiles = static_cast<int>(mt);
   g.n_tiles = static_cast<int>(nt);
@@ -464,20 +514,25 @@ cudaError_t run_pair(const LinearParams &p, cudaStream_t st) {
   g.k_steps = (p.K + S::kKStep - 1) / S::kKStep;
   g.out_block_tiles = (p.N + 127) / 128;
   g.has_residual = p.residual.data != nullptr;
+  if (HALVES == 2 && g.n_kb < kWideMinBlocks) return cudaErrorInvalidValue;
   static std::atomic<uint64_t> allowed;
-  const cudaError_t e = allow_shared(linear_pair_kernel<MX, BN, OUT8>, allowed, p.device, S::kSmemBytes);
+  const cudaError_t e = allow_shared(linear_pair_kernel<MX, BN, HALVES, OUT8>, allowed, p.device, S::kSmemBytes);
   if (e != cudaSuccess) return e;
   const int pairs = g.total < p.sms / 2 ? g.total : p.sms / 2;
-  linear_pair_kernel<MX, BN, OUT8><<<2 * pairs, S::kThreads, S::kSmemBytes, st>>>(p, g, tx, tw, tsx, tsw, tr, to);
+  linear_pair_kernel<MX, BN, HALVES, OUT8><<<2 * pairs, S::kThreads, S::kSmemBytes, st>>>(p, g, tx, tw, tsx, tsw, tr, to);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_linear_pair(const LinearParams &p, bool e4m3, bool out_e4m3, int bn, cudaStream_t st) {
-  if (e4m3) return out_e4m3 ? run_pair<true, 192, true>(p, st) : run_pair<true, 192, false>(p, st);
-  if (out_e4m3) return run_pair<false, 192, true>(p, st);
-  return bn == 256 ? run_pair<false, 256, false>(p, st) : run_pair<false, 192, false>(p, st);
+  if (bn == 384) {
+    if (e4m3) return out_e4m3 ? run_pair<true, 192, 2, true>(p, st) : run_pair<true, 192, 2, false>(p, st);
+    return out_e4m3 ? run_pair<false, 192, 2, true>(p, st) : run_pair<false, 192, 2, false>(p, st);
+  }
+  if (e4m3) return out_e4m3 ? run_pair<true, 192, 1, true>(p, st) : run_pair<true, 192, 1, false>(p, st);
+  if (out_e4m3) return run_pair<false, 192, 1, true>(p, st);
+  return bn == 256 ? run_pair<false, 256, 1, false>(p, st) : run_pair<false, 192, 1, false>(p, st);
 }
 
 }  // namespace wf

@@ -134,13 +134,14 @@ wf_status convert(const wf_rows *x, const wf_rows *out, bool to_e4m3, cudaStream
 }
 
 // Which kernel a product takes, and its tile: the smallest estimate of the time in
-// microseconds, from figures measured on a B200 at 1965 MHz with weights in HBM.
+// microseconds, from figures measured on a B200 (large products under its power
+// cap, small ones at 1965 MHz with weights in HBM).
 struct Plan {
   bool pair;
   int bn, nt, split;
 };
 
-Plan plan_linear(const LinearParams &p, bool e4m3, bool stored_by_tma) {
+Plan plan_linear(const LinearParams &p, bool e4m3, bool out8, bool stored_by_tma) {
   const int64_t n_kb = (static_cast<int64_t>(p.K) + (e4m3 ? 127 : 63)) / (e4m3 ? 128 : 64);
   const auto tiles = [](int64_t n, int64_t by) { return (n + by - 1) / by; };
   Plan best{false, 0, 0, 0};
@@ -153,13 +154,17 @@ Plan plan_linear(const LinearParams &p, bool e4m3, bool stored_by_tma) {
     }
   };
   if (stored_by_tma) {
-    // Waves of CTA pairs: a k-block of 128 bytes takes 0.26 (192 features) or
-    // 0.34 us (256), a tile no less than its epilogue's 2.5 us.
-    for (int bn = 192; bn <= (e4m3 ? 192 : 256); bn += 64) {
-      const double k_block = bn == 192 ? 0.26 : 0.34;
-      const int64_t waves = tiles(tiles(p.M, 256) * tiles(p.N, bn), p.sms / 2);
-      const double tile = n_kb * k_block;
-      offer(7.0 + waves * (tile > 2.5 ? tile : 2.5), Plan{true, bn, 0, 0});
+    // Waves of CTA pairs: a k-block of 128 bytes, and the part of a tile's epilogue
+    // that its neighbours' products do not cover; with SMs to spare the loads meet
+    // less traffic.
+    for (const int bn : {192, 256, 384}) {
+      if (bn == 256 && (e4m3 || out8)) continue;
+      if (bn == 384 && n_kb < kWideMinBlocks) continue;
+      const int64_t pairs = p.sms / 2, all = tiles(p.M, 256) * tiles(p.N, bn);
+      const double k_block = (e4m3 ? (bn == 192 ? 0.376 : 0.70) : bn == 192 ? 0.38 : bn == 256 ? 0.45 : 0.66) *
+                             (all <= pairs ? 0.72 : 1.0);
+      const double rest = e4m3 ? (bn == 192 ? 1.3 : 3.6) : bn == 192 ? 0.6 : bn == 256 ? 0.8 : 3.2;
+      offer(6.0 + tiles(all, pairs) * (n_kb * k_block + rest), Plan{true, bn, 0, 0});
     }
   }
   // Features on the M side: either the chain of k-blocks of a CTA (two CTAs per SM
@@ -279,7 +284,7 @@ wf_status wf_linear(const wf_rows *x, const wf_rows *w, const float *bias, int32
   p.sms = dev.sms;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool stored_by_tma = rows16(out) && (!residual || rows16(residual));
-  const Plan plan = plan_linear(p, e4m3, stored_by_tma);
+  const Plan plan = plan_linear(p, e4m3, out8, stored_by_tma);
   return status_of(plan.pair ? launch_linear_pair(p, e4m3, out8, plan.bn, st)
                              : launch_linear_skinny(p, e4m3, out8, plan.nt, plan.split, st));
 }

@@ -259,7 +259,10 @@ def test_linear_few_rows_bf16(n, features, k, act):
     assert wfb.rows_check_status() == 0
 
 
-PAIR = [(512, 1536, 512), (1111, 1000, 1544), (2000, 2048, 72), (2340, 1800, 200), (700, 5000, 64)]
+# Shapes that wf_linear's choice sends to every tile width of its many-row kernel (192, 256 and,
+# for long K, 384 features), ragged in every dimension.
+PAIR = [(512, 1536, 512), (1111, 1000, 1544), (2000, 2048, 72), (2340, 1800, 200), (700, 5000, 64),
+        (4600, 1528, 3000), (4601, 1000, 1032)]
 
 
 @pytest.mark.parametrize("n,features,k", PAIR)
@@ -286,7 +289,8 @@ def test_linear_few_rows_e4m3(n, features, k):
     assert wfb.rows_check_status() == 0
 
 
-PAIR8 = [(512, 1536, 512), (1111, 1000, 1184), (2000, 2048, 32), (2340, 1800, 224), (700, 5000, 96)]
+PAIR8 = [(512, 1536, 512), (1111, 1000, 1184), (2000, 2048, 32), (2340, 1800, 224), (700, 5000, 96),
+         (4600, 1528, 3008), (4601, 1496, 1056)]
 
 
 @pytest.mark.parametrize("n,features,k", PAIR8)
@@ -300,7 +304,8 @@ def test_linear_many_rows_e4m3(n, features, k):
 
 
 @pytest.mark.parametrize("e4m3", [False, True])
-@pytest.mark.parametrize("n,features,k", [(1, 96, 128), (30, 544, 288), (300, 64, 64), (1500, 1504, 320), (600, 6144, 128)])
+@pytest.mark.parametrize("n,features,k", [(1, 96, 128), (30, 544, 288), (300, 64, 64), (1500, 1504, 320), (600, 6144, 128),
+                                          (4600, 1504, 3008)])
 def test_linear_e4m3_output(n, features, k, e4m3):
     x, w, b = rows(n, k, 50), rows(features, k, 51, scale=k ** -0.5), vec(features, 52)
     xv = wv = None
