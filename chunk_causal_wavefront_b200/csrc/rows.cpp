@@ -180,7 +180,8 @@ Plan plan_linear(const LinearParams &p, bool e4m3, bool out8, bool stored_by_tma
     for (int split = 1; split <= 8 && split <= n_kb; split *= 2) {
       const double chain = static_cast<double>(tiles(n_kb, split)) * k_block + 0.05 * nt / split;
       double us = tiles(all * split, room) * chain;
-      const double l2 = all * n_kb * (16.0 + nt / 8.0) / 11e3, hbm = p.N * 128e-3 * n_kb / 6.5e3;
+      const double l2 = static_cast<double>(all) * n_kb * (16.0 + nt / 8.0) / 11e3;
+      const double hbm = p.N * 128e-3 * n_kb / 6.5e3;
       us = us > l2 ? us : l2;
       us = us > hbm ? us : hbm;
       offer(4.0 + us + (split == 8 ? 0.5 : 0.0), Plan{false, 0, nt, split});

@@ -314,9 +314,8 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const ConvertParams p) 
     const uint4 c = *reinterpret_cast<const uint4 *>(
         static_cast<const uint8_t *>(p.x.data) + static_cast<int64_t>(row) * p.x.ld + 16 * k);
     const int s = p.x.scales[scale_offset(row, static_cast<int>(k >> 1), block_tiles)];
-    // 2^(s - 127) as two factors, so that the ends of the byte's range are exact too.
-    const float f0 = __uint_as_float(static_cast<uint32_t>((s >> 1) + 64) << 23);
-    const float f1 = __uint_as_float(static_cast<uint32_t>(s - (s >> 1) + 63) << 23);
+    // 2^(s - 127); the byte of the smallest exponent, 0, is a subnormal float.
+    const float f2 = __uint_as_float(s ? static_cast<uint32_t>(s) << 23 : 0x400000u);
     const uint32_t w[4] = {c.x, c.y, c.z, c.w};
     float v[2][8];
 #pragma unroll
@@ -324,8 +323,8 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const ConvertParams p) 
       const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
           static_cast<__nv_fp8x2_storage_t>(w[j >> 1] >> (16 * (j & 1))), __NV_E4M3);
       const float2 f = __half22float2(__half2(h));
-      v[j >> 2][2 * (j & 3)] = f.x * f0 * f1;
-      v[j >> 2][2 * (j & 3) + 1] = f.y * f0 * f1;
+      v[j >> 2][2 * (j & 3)] = f.x * f2;
+      v[j >> 2][2 * (j & 3) + 1] = f.y * f2;
     }
     T *out = static_cast<T *>(p.out.data) + static_cast<int64_t>(row) * p.out.ld + 16 * k;
     if constexpr (VEC) {

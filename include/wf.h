@@ -385,7 +385,8 @@ enum { WF_ACT_NONE = 0, WF_ACT_GELU = 1, WF_ACT_SILU = 2 };
  * WF_ERR_INVALID_ARG unless cols is a positive multiple of 32. */
 wf_status wf_scale_bytes(int64_t rows, int64_t cols, size_t *bytes);
 
-/* out = x as E4M3 rows. x is bf16 or fp32, out E4M3 of the same shape. */
+/* out = x as E4M3 rows. x is bf16 or fp32, out E4M3 of the same shape, with
+ * rows * cols below 16 * 2^31 (WF_ERR_UNSUPPORTED otherwise, here and below). */
 wf_status wf_quantize_rows(const wf_rows *x, const wf_rows *out, wf_stream_t stream);
 
 /* out = the values that E4M3 rows stand for, as bf16 or fp32. Both are exact,

@@ -440,6 +440,110 @@ def test_streams_and_graphs():
             assert torch.equal(out[0], want[i][0]) and torch.equal(out[1], want[i][1])
 
 
+FIRST_CALL = """
+import torch, chunk_causal_wavefront_b200 as wf
+x = torch.ones(40, 256, device="cuda").bfloat16()
+w = torch.ones(512, 256, device="cuda").bfloat16()
+big, wide = torch.ones(2600, 256, device="cuda").bfloat16(), torch.ones(2048, 256, device="cuda").bfloat16()
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    y, s = wf.add_rms_norm(x, residual=x, out_dtype="e4m3")
+    z = wf.linear(y, wf.quantize_rows(w))
+    v = wf.linear(big, wide, act="silu")
+g.replay()
+torch.cuda.synchronize()
+assert (s == 2).all() and (z == 256).all() and (v == 256).all() and wf.rows_check_status() == 0
+print("first calls captured")
+"""
+
+
+def test_first_calls_of_a_process_can_be_captured():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "first calls captured" in r.stdout, r.stderr[-2000:]
+
+
+def test_two_streams_at_once():
+    """Few-row and many-row products and norms interleaved on two streams give what they give alone."""
+    x, w = rows(1400, 512, 94), rows(1536, 512, 95, scale=0.05)
+    few = [rows(n, 512, 96) for n in (1, 20, 90)]
+    x8, _ = quantized(x)
+    w8, _ = quantized(w)
+    calls = [lambda: wfb.linear(x, w), lambda: wfb.linear(few[0], w), lambda: wfb.linear(x8, w8),
+             lambda: wfb.linear(few[1], w, act="gelu"), lambda: wfb.add_rms_norm(x),
+             lambda: wfb.linear(few[2], w, out_dtype="e4m3").dequantize()]
+    want = [c() for c in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for rep in range(6):
+        for k, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                order = range(len(calls)) if k == 0 else reversed(range(len(calls)))
+                got += [(i, calls[i]()) for i in order]
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want[i]) for i, y in got)
+    assert wfb.rows_check_status() == 0
+
+
+def test_offsets_past_32_bits():
+    """Over 2^31 elements: the last rows match the same rows alone."""
+    n, cols = 425000, 5120
+    assert n * cols > 2 ** 31
+    x = torch.empty(n, cols, dtype=BF16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(7)
+    tail = torch.randn(256, cols, generator=g, device="cuda").bfloat16()
+    x[:256], x[-256:] = tail, tail
+    x[256:-256] = 1.0
+    out, s = wfb.add_rms_norm(x, residual=x)
+    want, ws = wfb.add_rms_norm(tail, residual=tail)
+    for a, b in ((out, want), (s, ws)):
+        assert torch.equal(a[-256:], b) and torch.equal(a[:256], b)
+    del out, s
+    q = wfb.quantize_rows(x)
+    wq = wfb.quantize_rows(tail).dequantize()
+    back = q.dequantize()
+    assert torch.equal(back[-256:], wq) and torch.equal(back[:256], wq) and (back[300:-300] == 1).all()
+    del back
+    w = rows(64, cols, 97, scale=cols ** -0.5)
+    want = wfb.linear(tail, w)
+    for got in (wfb.linear(x, w), wfb.linear(x, w[:63])):      # stored by TMA, and not
+        k = got.shape[1]
+        err = (got[-256:].float() - want[:, :k].float()).abs().max()
+        assert err <= 2 ** -7 * want.abs().max() and torch.equal(got[:256], got[-256:])
+    w8 = wfb.quantize_rows(w)
+    got = wfb.linear(q, w8)
+    assert torch.equal(got[:256], got[-256:])
+    del x, q
+    small, wide = rows(110000, 64, 98), rows(20480, 64, 99, scale=0.125)
+    y = wfb.linear(small, wide)
+    assert y.numel() > 2 ** 31
+    want = R.linear(f64(small[-64:]), f64(wide), None, "none", None)
+    assert (np.abs(f64(y[-64:]) - want) <= np.abs(want) * 2.0 ** -8 + 1e-4).all()
+    assert wfb.rows_check_status() == 0
+
+
+def test_operands_may_share_memory():
+    x = rows(300, 256, 100)
+    check_linear(x, x, None, "none", None, wfb.linear(x, x))
+    q, v = quantized(x)
+    check_linear(q, q, None, "none", None, wfb.linear(q, q), v, v)
+    buf = rows(200, 768, 101)
+    a, b = buf[:, :256], buf[:, 256:768]
+    w = rows(512, 256, 102, scale=1 / 16)
+    want = wfb.linear(a, w)
+    wfb.linear(a, w, out=b)                                   # a column range beside its input
+    assert torch.equal(b, want)
+    with pytest.raises(wfb.WfError):
+        wfb.linear(a, w, out=buf[:, 128:640])
+    out, s = wfb.add_rms_norm(x, residual=x)
+    assert torch.equal(s, (2 * x.float()).bfloat16())
+
+
 def test_refusals_on_device():
     x, w = rows(4, 64, 90), rows(8, 64, 91)
     with pytest.raises(ValueError, match="one device"):
