@@ -80,6 +80,12 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
+// 1 / sqrt(mean + eps), once per row in 64 bits and rounded once: a row's elements
+// share this factor's error, which could carry many of them over an E4M3 rounding.
+__device__ __forceinline__ float norm_scale(float ss, double inv_cols, float eps) {
+  return static_cast<float>(rsqrt(static_cast<double>(ss) * inv_cols + static_cast<double>(eps)));
+}
+
 // Largest magnitude; fmaxf leaves NaN out.
 __device__ __forceinline__ float amax8(const float (&v)[8]) {
   float m = 0.f;
@@ -93,14 +99,14 @@ __device__ __forceinline__ float amax8(const float (&v)[8]) {
 // are reduced, so that loads are in flight at every barrier. Outputs may be the
 // inputs: a chunk is stored by the thread that loaded it, and rows do not overlap.
 template <typename T, bool OUT8, int CH>
-__global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormParams p, const int wpr) {
+__global__ void __launch_bounds__(kNormThreads, sizeof(T) == 2 && CH < 4 ? 3 : 2) norm_kernel(const NormParams p, const int wpr) {
   __shared__ float part[2][kNormThreads / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = warp / wpr;                      // row of the block's pass
   const int rows = blockDim.x / 32 / wpr;
   const int t = (warp - sub * wpr) * 32 + lane;    // thread of the row
   const int chunks = p.cols >> 3, stride = 32 * wpr;
-  const float inv = 1.0f / static_cast<float>(p.cols);
+  const double inv = 1.0 / p.cols;
   const int block_tiles = (p.cols + 127) >> 7;
   const T *x = static_cast<const T *>(p.x.data), *r = static_cast<const T *>(p.residual.data);
   typename RawOf<T>::type rx[CH] = {}, rr[CH] = {};
@@ -146,7 +152,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormParams p, 
       ss = 0.f;
       for (int i = 0; i < wpr; ++i) ss += part[turn][sub * wpr + i];
     }
-    const float scale = 1.0f / sqrtf(ss * inv + p.eps);
+    const float scale = norm_scale(ss, inv, p.eps);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int k = t + c * stride;
@@ -195,7 +201,7 @@ template <typename T, bool OUT8, bool KEEP>
 __global__ void __launch_bounds__(kAnyThreads) norm_any_kernel(const NormParams p) {
   __shared__ float part[2][kAnyThreads / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const float inv = 1.0f / static_cast<float>(p.cols);
+  const double inv = 1.0 / p.cols;
   const int block_tiles = (p.cols + 127) >> 7;
   int turn = 0;
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
@@ -235,7 +241,7 @@ __global__ void __launch_bounds__(kAnyThreads) norm_any_kernel(const NormParams 
     ss = 0.f;
 #pragma unroll
     for (int i = 0; i < kAnyThreads / 32; ++i) ss += part[turn][i];
-    const float scale = 1.0f / sqrtf(ss * inv + p.eps);
+    const float scale = norm_scale(ss, inv, p.eps);
     // cols is a multiple of 32 for E4M3, so a warp is wholly in or out there.
     auto finish = [&](int64_t k, float s) {
       const float v = s * scale * (p.weight ? __ldg(p.weight + k) : 1.0f);
