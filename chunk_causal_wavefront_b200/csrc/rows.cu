@@ -2,6 +2,10 @@
 // fp32, for sm_100a.
 //
 // All three read each element once and write each result once; HBM bounds them.
+// Measured, of the 6554 GB/s that a copy reaches: norm with residual, 23400 x 1536
+// bf16 48.5 us (90 %), 23400 x 5120 to E4M3 139 us (93 %); without residual 27.4 us
+// (80 %: half the bytes in flight per row); 23400 x 5120 bf16 to E4M3 60 us (92 %)
+// and back 62 us (90 %); a single row 2.7 us, all of it launch and latency.
 //
 // Norm: s = x + residual, out = s / sqrt(mean(s^2) + eps) * weight.
 //   A row stays in registers between its one read and its one write: up to 8
@@ -99,7 +103,7 @@ __device__ __forceinline__ float amax8(const float (&v)[8]) {
 // are reduced, so that loads are in flight at every barrier. Outputs may be the
 // inputs: a chunk is stored by the thread that loaded it, and rows do not overlap.
 template <typename T, bool OUT8, int CH>
-__global__ void __launch_bounds__(kNormThreads, sizeof(T) == 2 && CH < 4 ? 3 : 2) norm_kernel(const NormParams p, const int wpr) {
+__global__ void __launch_bounds__(kNormThreads, (sizeof(T) == 2 ? 2 : 1) + (CH < 4)) norm_kernel(const NormParams p, const int wpr) {
   __shared__ float part[2][kNormThreads / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = warp / wpr;                      // row of the block's pass
