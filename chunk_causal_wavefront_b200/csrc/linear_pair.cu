@@ -42,6 +42,10 @@
 //                      bias goes through 32 floats of shared memory per warp.
 //                      E4M3 output: the 32 columns are one scale block, so a
 //                      thread finds its scale without leaving its registers.
+//   Output or residual rows that TMA cannot reach (an odd N, a stride that is not a
+//   multiple of 16 bytes) take DIRECT: the staging rows are written and read with
+//   a lane per column, 64 bytes of a row at a time; 23400 x 1535 x 1536 bf16 100 us, with
+//   residual 140 (1536 features through TMA: 87).
 // Every wait is bounded; a timeout is recorded in the row-operator status word.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -117,7 +121,7 @@ __device__ __forceinline__ void decode(const PairGrid &g, int t, int &mt, int &n
   mt = grp * kGroup + (r - nt * gm);
 }
 
-template <bool MX, int BN, int HALVES, bool OUT8>
+template <bool MX, int BN, int HALVES, bool OUT8, bool DIRECT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MX, BN, HALVES>::kThreads, 1)
     linear_pair_kernel(const __grid_constant__ LinearParams p, const __grid_constant__ PairGrid g,
                        const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw,
@@ -317,7 +321,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MX, BN, HALVES
     int buf = 0;
     int row0, tile_col, row1, tile_col1;                 // this tile's and the next one's place
     place(0, row1, tile_col1);
-    if (g.has_residual && lane == 0) fetch(row1, tile_col1, 0);
+    if (!DIRECT && g.has_residual && lane == 0) fetch(row1, tile_col1, 0);
     float bias = bias_at(tile_col1);
     bool ok = true;
     const int tiles = (g.total - pair + npairs - 1) / npairs;
@@ -343,12 +347,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MX, BN, HALVES
         const int next_row = same ? row0 : row1, next_col = same ? col0 + 32 : tile_col1;
         const int buf1 = buf + 1 == S::kBufs ? 0 : buf + 1;
         // Stores of buf (kBufs steps ago) and buf1 (one step fewer) have been read.
-        if (lane == 0) {
+        if (!DIRECT && lane == 0) {
           asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(S::kBufs - 2) : "memory");
           if (g.has_residual) fetch(next_row, next_col, buf1);
         }
         bias_row[lane] = bias;
         bias = bias_at(next_col);
+        // DIRECT: the residual's box, lane = column, all rows in flight at once; places
+        // outside are clamped into it.
+        uint16_t res_rows[DIRECT ? 32 : 1];
+        if constexpr (DIRECT) {
+          if (g.has_residual && on) {
+            const int col = col0 + lane < p.N ? col0 + lane : p.N - 1;
+            const uint16_t *r = static_cast<const uint16_t *>(p.residual.data) + col;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              res_rows[j] = r[static_cast<int64_t>(row0 + j < p.M ? row0 + j : p.M - 1) * p.residual.ld];
+          }
+        }
         __syncwarp();
         if (on) {
           float v[32];
@@ -371,6 +387,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MX, BN, HALVES
           // j ^ (r / 2 % 4).
           const uint32_t addr = smem_u32(bufs + buf * kBufBytes + lane * 64);
           const uint32_t x = (lane >> 1) & 3;
+          auto staged = [&](int r, int c) {               // bf16 column c of row r
+            return bufs + buf * kBufBytes + r * 64 + (((c >> 3) ^ ((r >> 1) & 3)) << 4) + (c & 7) * 2;
+          };
           if constexpr (OUT8) {
             // The warpgroup's 64 columns share a staging row: two scale blocks.
             float m = 0.f;
@@ -395,10 +414,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MX, BN, HALVES
                   static_cast<uint8_t>(ex + 127);
           } else {
             if (g.has_residual) {
-              ok = __all_sync(0xffffffffu, wait_bar(ctx, res_bar + buf, (res_phase >> buf) & 1));
-              if (!ok) break;
-              res_phase ^= 1u << buf;
-              res_pending &= ~(1u << buf);
+              if constexpr (DIRECT) {
+                // The staging rows turn the residual's columns around.
+#pragma unroll
+                for (int j = 0; j < 32; ++j) *reinterpret_cast<uint16_t *>(staged(j, lane)) = res_rows[j];
+                __syncwarp();
+              } else {
+                ok = __all_sync(0xffffffffu, wait_bar(ctx, res_bar + buf, (res_phase >> buf) & 1));
+                if (!ok) break;
+                res_phase ^= 1u << buf;
+                res_pending &= ~(1u << buf);
+              }
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 uint32_t w[4];
@@ -425,10 +451,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MX, BN, HALVES
                            : "memory");
             }
           }
-          fence_proxy_async_smem();
+          if constexpr (DIRECT) {
+            __syncwarp();
+            uint16_t *o = static_cast<uint16_t *>(p.out.data) + static_cast<int64_t>(row0) * p.out.ld + col0 + lane;
+#pragma unroll 8
+            for (int j = 0; j < 32; ++j)
+              if (row0 + j < p.M && col0 + lane < p.N)
+                o[j * p.out.ld] = *reinterpret_cast<const uint16_t *>(staged(j, lane));
+          } else {
+            fence_proxy_async_smem();
+          }
         }
         __syncwarp();
-        if constexpr (OUT8) {
+        if constexpr (DIRECT) {
+          // The one staging buffer is free again.
+        } else if constexpr (OUT8) {
           // One store for both steps; columns past N are clipped.
           if (c + 1 == kSteps) {
             if (lane == 0) {
@@ -476,7 +513,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MX, BN, HALVES
   }
 }
 
-template <bool MX, int BN, int HALVES, bool OUT8>
+template <bool MX, int BN, int HALVES, bool OUT8, bool DIRECT>
 cudaError_t run_pair(const LinearParams &p, cudaStream_t st) {
   using S = Shape<MX, BN, HALVES>;
   const int elt = MX ? 1 : 2;
@@ -496,12 +533,14 @@ cudaError_t run_pair(const LinearParams &p, cudaStream_t st) {
     ok = ok && encode_rows_map(&tsx, 4, 0, p.x.scales, 3, sd, ss, sb) &&
          encode_rows_map(&tsw, 4, 0, p.w.scales, 3, qd, ss, qb);
   }
-  const int oelt = OUT8 ? 1 : 2;
-  const uint64_t os[1] = {static_cast<uint64_t>(p.out.ld) * oelt};
-  ok = ok && encode_rows_map(&to, oelt, 64, p.out.data, 2, od, os, ob);
-  if (p.residual.data) {
-    const uint64_t rs[1] = {static_cast<uint64_t>(p.residual.ld) * 2};
-    ok = ok && encode_rows_map(&tr, 2, 64, p.residual.data, 2, od, rs, ob);
+  if (!DIRECT) {
+    const int oelt = OUT8 ? 1 : 2;
+    const uint64_t os[1] = {static_cast<uint64_t>(p.out.ld) * oelt};
+    ok = ok && encode_rows_map(&to, oelt, 64, p.out.data, 2, od, os, ob);
+    if (p.residual.data) {
+      const uint64_t rs[1] = {static_cast<uint64_t>(p.residual.ld) * 2};
+      ok = ok && encode_rows_map(&tr, 2, 64, p.residual.data, 2, od, rs, ob);
+    }
   }
   if (!ok) return cudaErrorInvalidValue;
   PairGrid g{};
@@ -516,23 +555,31 @@ cudaError_t run_pair(const LinearParams &p, cudaStream_t st) {
   g.has_residual = p.residual.data != nullptr;
   if (HALVES == 2 && g.n_kb < kWideMinBlocks) return cudaErrorInvalidValue;
   static std::atomic<uint64_t> allowed;
-  const cudaError_t e = allow_shared(linear_pair_kernel<MX, BN, HALVES, OUT8>, allowed, p.device, S::kSmemBytes);
+  const cudaError_t e = allow_shared(linear_pair_kernel<MX, BN, HALVES, OUT8, DIRECT>, allowed, p.device, S::kSmemBytes);
   if (e != cudaSuccess) return e;
   const int pairs = g.total < p.sms / 2 ? g.total : p.sms / 2;
-  linear_pair_kernel<MX, BN, HALVES, OUT8><<<2 * pairs, S::kThreads, S::kSmemBytes, st>>>(p, g, tx, tw, tsx, tsw, tr, to);
+  linear_pair_kernel<MX, BN, HALVES, OUT8, DIRECT><<<2 * pairs, S::kThreads, S::kSmemBytes, st>>>(p, g, tx, tw, tsx, tsw, tr, to);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_linear_pair(const LinearParams &p, bool e4m3, bool out_e4m3, int bn, cudaStream_t st) {
-  if (bn == 384) {
-    if (e4m3) return out_e4m3 ? run_pair<true, 192, 2, true>(p, st) : run_pair<true, 192, 2, false>(p, st);
-    return out_e4m3 ? run_pair<false, 192, 2, true>(p, st) : run_pair<false, 192, 2, false>(p, st);
+cudaError_t launch_linear_pair(const LinearParams &p, bool e4m3, bool out_e4m3, bool direct, int bn,
+                               cudaStream_t st) {
+  if (out_e4m3) {
+    if (e4m3) return bn == 384 ? run_pair<true, 192, 2, true, false>(p, st) : run_pair<true, 192, 1, true, false>(p, st);
+    return bn == 384 ? run_pair<false, 192, 2, true, false>(p, st) : run_pair<false, 192, 1, true, false>(p, st);
   }
-  if (e4m3) return out_e4m3 ? run_pair<true, 192, 1, true>(p, st) : run_pair<true, 192, 1, false>(p, st);
-  if (out_e4m3) return run_pair<false, 192, 1, true>(p, st);
-  return bn == 256 ? run_pair<false, 256, 1, false>(p, st) : run_pair<false, 192, 1, false>(p, st);
+  if (direct) {
+    if (e4m3) return bn == 384 ? run_pair<true, 192, 2, false, true>(p, st) : run_pair<true, 192, 1, false, true>(p, st);
+    return bn == 384   ? run_pair<false, 192, 2, false, true>(p, st)
+           : bn == 256 ? run_pair<false, 256, 1, false, true>(p, st)
+                       : run_pair<false, 192, 1, false, true>(p, st);
+  }
+  if (e4m3) return bn == 384 ? run_pair<true, 192, 2, false, false>(p, st) : run_pair<true, 192, 1, false, false>(p, st);
+  return bn == 384   ? run_pair<false, 192, 2, false, false>(p, st)
+         : bn == 256 ? run_pair<false, 256, 1, false, false>(p, st)
+                     : run_pair<false, 192, 1, false, false>(p, st);
 }
 
 }  // namespace wf

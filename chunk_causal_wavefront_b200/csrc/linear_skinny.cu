@@ -1,5 +1,5 @@
-// Matrix product with bias, activation and residual for sm_100a, few rows (and
-// any shape whose output rows TMA cannot store): features on the M side.
+// Matrix product with bias, activation and residual for sm_100a, few rows: features
+// on the M side.
 //
 // The bytes of w bound it: with few rows every weight is used only a few times.
 // So w streams through the tensor core as the A operand, 128 features per tile,

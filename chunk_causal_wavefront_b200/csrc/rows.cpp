@@ -141,7 +141,7 @@ struct Plan {
   int bn, nt, split;
 };
 
-Plan plan_linear(const LinearParams &p, bool e4m3, bool out8, bool stored_by_tma) {
+Plan plan_linear(const LinearParams &p, bool e4m3, bool out8) {
   const int64_t n_kb = (static_cast<int64_t>(p.K) + (e4m3 ? 127 : 63)) / (e4m3 ? 128 : 64);
   const auto tiles = [](int64_t n, int64_t by) { return (n + by - 1) / by; };
   Plan best{false, 0, 0, 0};
@@ -153,19 +153,17 @@ Plan plan_linear(const LinearParams &p, bool e4m3, bool out8, bool stored_by_tma
       best = plan;
     }
   };
-  if (stored_by_tma) {
-    // Waves of CTA pairs: a k-block of 128 bytes, and the part of a tile's epilogue
-    // that its neighbours' products do not cover; with SMs to spare the loads meet
-    // less traffic.
-    for (const int bn : {192, 256, 384}) {
-      if (bn == 256 && (e4m3 || out8)) continue;
-      if (bn == 384 && n_kb < kWideMinBlocks) continue;
-      const int64_t pairs = p.sms / 2, all = tiles(p.M, 256) * tiles(p.N, bn);
-      const double k_block = (e4m3 ? (bn == 192 ? 0.376 : 0.70) : bn == 192 ? 0.38 : bn == 256 ? 0.45 : 0.66) *
-                             (all <= pairs ? 0.72 : 1.0);
-      const double rest = e4m3 ? (bn == 192 ? 1.3 : 3.6) : bn == 192 ? 0.6 : bn == 256 ? 0.8 : 3.2;
-      offer(6.0 + tiles(all, pairs) * (n_kb * k_block + rest), Plan{true, bn, 0, 0});
-    }
+  // Waves of CTA pairs: a k-block of 128 bytes, and the part of a tile's epilogue
+  // that its neighbours' products do not cover; with SMs to spare the loads meet
+  // less traffic.
+  for (const int bn : {192, 256, 384}) {
+    if (bn == 256 && (e4m3 || out8)) continue;
+    if (bn == 384 && n_kb < kWideMinBlocks) continue;
+    const int64_t pairs = p.sms / 2, all = tiles(p.M, 256) * tiles(p.N, bn);
+    const double k_block = (e4m3 ? (bn == 192 ? 0.376 : 0.70) : bn == 192 ? 0.38 : bn == 256 ? 0.45 : 0.66) *
+                           (all <= pairs ? 0.72 : 1.0);
+    const double rest = e4m3 ? (bn == 192 ? 1.3 : 3.6) : bn == 192 ? 0.6 : bn == 256 ? 0.8 : 3.2;
+    offer(6.0 + tiles(all, pairs) * (n_kb * k_block + rest), Plan{true, bn, 0, 0});
   }
   // Features on the M side: either the chain of k-blocks of a CTA (two CTAs per SM
   // up to 64 tokens) and its epilogue, or the bytes that all tiles read through L2
@@ -285,8 +283,8 @@ wf_status wf_linear(const wf_rows *x, const wf_rows *w, const float *bias, int32
   p.sms = dev.sms;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool stored_by_tma = rows16(out) && (!residual || rows16(residual));
-  const Plan plan = plan_linear(p, e4m3, out8, stored_by_tma);
-  return status_of(plan.pair ? launch_linear_pair(p, e4m3, out8, plan.bn, st)
+  const Plan plan = plan_linear(p, e4m3, out8);
+  return status_of(plan.pair ? launch_linear_pair(p, e4m3, out8, !stored_by_tma, plan.bn, st)
                              : launch_linear_skinny(p, e4m3, out8, plan.nt, plan.split, st));
 }
 

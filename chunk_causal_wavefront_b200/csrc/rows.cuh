@@ -48,13 +48,13 @@ enum class RowsType { kBf16, kF32, kE4m3 };
 cudaError_t launch_add_rms_norm(const NormParams &p, RowsType in, bool out_e4m3, cudaStream_t st);
 cudaError_t launch_quantize_rows(const ConvertParams &p, RowsType in, cudaStream_t st);
 cudaError_t launch_dequantize_rows(const ConvertParams &p, RowsType out, cudaStream_t st);
-// Large products, on CTA pairs: out and residual rows 16-byte aligned. bn: 192, 256
-// (bf16 to bf16 only) or 384 features per tile, the last for at least kWideMinBlocks
-// k-blocks of 128 bytes.
+// Large products, on CTA pairs. bn: 192, 256 (bf16 to bf16 only) or 384 features per
+// tile, the last for at least kWideMinBlocks k-blocks of 128 bytes. direct: bf16
+// output or residual rows are not 16-byte aligned.
 constexpr int kWideMinBlocks = 8;
-cudaError_t launch_linear_pair(const LinearParams &p, bool e4m3, bool out_e4m3, int bn,
+cudaError_t launch_linear_pair(const LinearParams &p, bool e4m3, bool out_e4m3, bool direct, int bn,
                                cudaStream_t st);
-// Few rows, ragged or unaligned outputs: features on the MMA's M side, K split
+// Few rows: features on the MMA's M side, K split
 // over a cluster of `split` CTAs, `nt` tokens per tile.
 cudaError_t launch_linear_skinny(const LinearParams &p, bool e4m3, bool out_e4m3, int nt,
                                  int split, cudaStream_t st);

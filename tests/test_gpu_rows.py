@@ -262,7 +262,9 @@ def test_linear_few_rows_bf16(n, features, k, act):
 # Shapes that wf_linear's choice sends to every tile width of its many-row kernel (192, 256 and,
 # for long K, 384 features), ragged in every dimension.
 PAIR = [(512, 1536, 512), (1111, 1000, 1544), (2000, 2048, 72), (2340, 1800, 200), (700, 5000, 64),
-        (4600, 1528, 3000), (4601, 1000, 1032)]
+        (4600, 1528, 3000), (4601, 1000, 1032),
+        # output rows that TMA cannot store
+        (2340, 1801, 200), (4600, 1527, 3000), (4601, 1001, 1032), (1500, 4999, 64)]
 
 
 @pytest.mark.parametrize("n,features,k", PAIR)
@@ -290,7 +292,8 @@ def test_linear_few_rows_e4m3(n, features, k):
 
 
 PAIR8 = [(512, 1536, 512), (1111, 1000, 1184), (2000, 2048, 32), (2340, 1800, 224), (700, 5000, 96),
-         (4600, 1528, 3008), (4601, 1496, 1056)]
+         (4600, 1528, 3008), (4601, 1496, 1056),
+         (2340, 1801, 224), (4600, 1527, 3008), (2000, 2047, 32)]
 
 
 @pytest.mark.parametrize("n,features,k", PAIR8)
@@ -328,7 +331,7 @@ def test_linear_strides_and_untouched_memory(n, ldo):
     assert (big[:2] == 5).all() and (big[n + 2:] == 5).all() and (big[:, features:] == 5).all()
 
 
-@pytest.mark.parametrize("n,features", [(9, 130), (1300, 1536)])
+@pytest.mark.parametrize("n,features", [(9, 130), (1300, 1536), (2600, 1535)])
 def test_linear_in_place_on_the_residual(n, features):
     x, w, r = rows(n, 256, 56), rows(features, 256, 57, scale=1 / 16), rows(n, features, 58)
     want = wfb.linear(x, w, residual=r)
