@@ -1,4 +1,5 @@
-"""Build libwf.so in-tree with nvcc for sm_100a.
+"""Build libwf.so in-tree with nvcc for sm_100a, and the row operators' torch binding
+(_rows_bind.so) with the host compiler.
 
 Usage: python chunk_causal_wavefront_b200/build.py [--force] [--verbose] [--ptxas-info]
 (run by path, so that a stale libwf.so is not loaded through the package)
@@ -7,10 +8,12 @@ from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +21,9 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libwf.so")
+
+BIND_SRC = os.path.join(PKG, "bind", "rows_bind.cpp")
+BIND = os.path.join(PKG, "_rows_bind.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O3", "-I", INCLUDE, "-I", CSRC]
@@ -56,6 +62,31 @@ def _compile(src: str, verbose: bool, extra) -> str:
     return obj
 
 
+def build_bind(force: bool = False, verbose: bool = False) -> str:
+    """The compiled common case of the row operators' torch-facing calls, against the installed
+    torch's headers (found without importing it)."""
+    deps = [BIND_SRC, os.path.join(INCLUDE, "wf.h")]
+    if not force and os.path.exists(BIND) and os.path.getmtime(BIND) >= max(map(os.path.getmtime, deps)):
+        return BIND
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    system = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+              cuda, sysconfig.get_paths()["include"]]
+    tmp = BIND + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE]
+    for d in system:
+        cmd += ["-isystem", d]
+    cmd += [BIND_SRC, "-o", tmp, "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch",
+            "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"building {BIND_SRC} failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BIND)
+    return BIND
+
+
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     os.makedirs(BUILD, exist_ok=True)
     if force:
@@ -76,6 +107,7 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    build_bind(force, verbose)
     return LIB
 
 

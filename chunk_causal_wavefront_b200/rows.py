@@ -14,6 +14,8 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib
+import importlib.util
 import math
 import struct
 from typing import Optional, Tuple, Union
@@ -91,6 +93,10 @@ class E4M3Rows:
     def dequantize(self, out: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.bfloat16,
                    stream=None) -> torch.Tensor:
         """The values these rows stand for, as bf16 or fp32 (exact in both)."""
+        if _fast is not None and out is None and stream is None and dtype in _TYPES:
+            r = _fast.dequantize_rows(self.codes, self.scales, dtype is torch.float32)
+            if r is not NotImplemented:
+                return r if type(r) is not int else _check(r, "wf_dequantize_rows")
         raw = _here(stream, self, out)
         if raw is None:
             with _elsewhere(self.device, stream):
@@ -151,6 +157,21 @@ def _entry(name: str):
 
 _quantize, _dequantize = _entry("wf_quantize_rows"), _entry("wf_dequantize_rows")
 _norm, _linear = _entry("wf_add_rms_norm"), _entry("wf_linear")
+
+# The compiled common case (contiguous tensors on the current device, outputs to be
+# allocated, current stream): the same library calls with less of the host's time.
+# It answers NotImplemented where the code below has to check, refuse or convert;
+# without the built module that code serves every call.
+_fast = None
+if importlib.util.find_spec(__package__ + "._rows_bind") is not None:
+    _fast = importlib.import_module(__package__ + "._rows_bind")
+    _fast.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (_linear, _norm, _quantize, _dequantize)))
+
+
+def _made(codes: torch.Tensor, scales: torch.Tensor) -> "E4M3Rows":
+    out = E4M3Rows.__new__(E4M3Rows)
+    out.codes, out.scales = codes, scales
+    return out
 
 
 def _check(status: int, what: str) -> None:
@@ -213,10 +234,8 @@ def _new(like: torch.Tensor, shape, out_dtype, default: torch.dtype) -> Operand:
         rows, cols = math.prod(shape[:-1]), shape[-1]
         if cols % 32:
             raise ValueError("E4M3 rows need a multiple of 32 columns")
-        out = E4M3Rows.__new__(E4M3Rows)
-        out.codes = like.new_empty((rows, cols), dtype=torch.float8_e4m3fn)
-        out.scales = like.new_empty((rows + 127) // 128 * ((cols + 127) // 128) * 512, dtype=torch.uint8)
-        return out
+        return _made(like.new_empty((rows, cols), dtype=torch.float8_e4m3fn),
+                     like.new_empty((rows + 127) // 128 * ((cols + 127) // 128) * 512, dtype=torch.uint8))
     raise ValueError(f"out_dtype must be {default} (the default) or 'e4m3'")
 
 
@@ -226,6 +245,10 @@ def _packed_like(x: torch.Tensor) -> torch.Tensor:
 
 def quantize_rows(x: torch.Tensor, out: Optional[E4M3Rows] = None, stream=None) -> E4M3Rows:
     """x [..., cols] in bf16 or fp32 as E4M3 rows (leading dimensions flattened)."""
+    if _fast is not None and out is None and stream is None:
+        r = _fast.quantize_rows(x)
+        if r is not NotImplemented:
+            return _made(*r) if type(r) is not int else _check(r, "wf_quantize_rows")
     raw = _here(stream, x, out)
     if raw is None:
         with _elsewhere(x.device, stream):
@@ -245,6 +268,15 @@ def add_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *,
     E4M3Rows with out_dtype="e4m3" (or out=E4M3Rows). sum_out may be x or
     residual: the residual stream is then updated in place. weight is float32.
     """
+    if (_fast is not None and out is None and sum_out is None and stream is None
+            and (out_dtype is None or out_dtype == "e4m3")):
+        r = _fast.add_rms_norm(x, weight, residual, eps, out_dtype is not None)
+        if r is not NotImplemented:
+            if type(r) is int:
+                _check(r, "wf_add_rms_norm")
+            if out_dtype is None:
+                return r
+            return _made(*r) if residual is None else (_made(r[0], r[1]), r[2])
     shape = x.shape
     if residual is None:
         if sum_out is not None:
@@ -292,6 +324,16 @@ def linear(x: Operand, w: Operand, bias: Optional[torch.Tensor] = None, *, act: 
     code = _ACTS.get(act)
     if code is None:
         raise ValueError(f"act must be one of {sorted(_ACTS)}")
+    if (_fast is not None and out is None and stream is None
+            and (out_dtype is None or out_dtype == "e4m3")):
+        if type(x) is E4M3Rows and type(w) is E4M3Rows:
+            r = _fast.linear(x.codes, x.scales, w.codes, w.scales, bias, code, residual, out_dtype is not None)
+        else:
+            r = _fast.linear(x, None, w, None, bias, code, residual, out_dtype is not None)
+        if r is not NotImplemented:
+            if type(r) is int:
+                _check(r, "wf_linear")
+            return r if out_dtype is None else _made(*r)
     xs, ws = x.shape, w.shape
     if len(ws) != 2 or not xs or xs[-1] != ws[1]:
         raise ValueError(f"shapes {tuple(xs)} and {tuple(ws)} do not give x w^T")

@@ -547,6 +547,55 @@ def test_operands_may_share_memory():
     assert torch.equal(s, (2 * x.float()).bfloat16())
 
 
+def test_compiled_calls_are_the_python_calls(monkeypatch):
+    """The compiled common case gives the bits of the Python path, and leaves it what it does not take."""
+    from chunk_causal_wavefront_b200 import rows as PR
+    assert PR._fast is not None, "_rows_bind.so is not built"
+    x, r, w = rows(37, 256, 110), rows(37, 256, 111), rows(96, 256, 112, scale=1 / 16)
+    wt, b, r2 = vec(256, 113, 1.0), vec(96, 114), rows(37, 96, 115)
+    nd = x.view(37, 4, 64)
+    x8, w8 = wfb.quantize_rows(x), wfb.quantize_rows(w)
+    calls = [
+        lambda: wfb.add_rms_norm(x), lambda: wfb.add_rms_norm(x.float(), wt, residual=r.float(), eps=1e-3),
+        lambda: wfb.add_rms_norm(x, wt, residual=r, out_dtype="e4m3"), lambda: wfb.add_rms_norm(x, out_dtype="e4m3"),
+        lambda: wfb.add_rms_norm(nd), lambda: wfb.add_rms_norm(x[:, :128]), lambda: wfb.add_rms_norm(x[:0], residual=x[:0]),
+        lambda: wfb.linear(x, w), lambda: wfb.linear(x, w, b, act="gelu", residual=r2),
+        lambda: wfb.linear(x, w, out_dtype="e4m3"), lambda: wfb.linear(x8, w8, b, act="silu", residual=r2),
+        lambda: wfb.linear(x8, w8, out_dtype="e4m3"), lambda: wfb.linear(nd, w[:, :64].contiguous()),
+        lambda: wfb.linear(x[:, :128], w[:, :128]), lambda: wfb.linear(x, w, out_dtype=torch.bfloat16),
+        lambda: wfb.linear(x[0], w), lambda: wfb.linear(x[:0], w), lambda: wfb.linear(x8.first(9), w8),
+        lambda: wfb.quantize_rows(nd), lambda: x8.dequantize(), lambda: x8.dequantize(dtype=F32),
+    ]
+    bad = [lambda: wfb.linear(x, w[:, :64]), lambda: wfb.linear(x, w, b[:5]), lambda: wfb.linear(x, w8),
+           lambda: wfb.linear(x8, w), lambda: wfb.linear(x, w, residual=r), lambda: wfb.linear(x.float(), w.float()),
+           lambda: wfb.linear(x, w, residual=r2, out_dtype="e4m3"), lambda: wfb.linear(x, w[:33], out_dtype="e4m3"),
+           lambda: wfb.add_rms_norm(x, b), lambda: wfb.add_rms_norm(x, residual=r2), lambda: wfb.add_rms_norm(x, eps=-1.0),
+           lambda: wfb.add_rms_norm(x, eps=float("nan")), lambda: wfb.add_rms_norm(x.half()), lambda: wfb.linear(x.cpu(), w),
+           lambda: wfb.quantize_rows(x[:, :40].contiguous()), lambda: wfb.linear(x.clone().requires_grad_(), w),
+           lambda: wfb.linear(x, None), lambda: wfb.add_rms_norm(x, "w"), lambda: x8.dequantize(dtype=torch.float16)]
+
+    def flat(v):
+        if isinstance(v, tuple):
+            return [t for u in v for t in flat(u)]
+        return [v.codes.view(torch.uint8), v.dequantize()] if isinstance(v, wfb.E4M3Rows) else [v]
+
+    fast, fast_errors = [flat(c()) for c in calls], []
+    for c in bad:
+        with pytest.raises(Exception) as e:
+            c()
+        fast_errors.append((type(e.value), str(e.value)))
+    monkeypatch.setattr(PR, "_fast", None)
+    for c, want in zip(calls, fast):
+        got = flat(c())
+        assert len(got) == len(want)
+        for g, v in zip(got, want):
+            assert g.shape == v.shape and g.dtype == v.dtype and torch.equal(g, v)
+    for c, want in zip(bad, fast_errors):
+        with pytest.raises(Exception) as e:
+            c()
+        assert (type(e.value), str(e.value)) == want
+
+
 def test_refusals_on_device():
     x, w = rows(4, 64, 90), rows(8, 64, 91)
     with pytest.raises(ValueError, match="one device"):
