@@ -74,6 +74,7 @@ __global__ void __launch_bounds__(kThreads)
   using S = Shape<MX, NT>;
   constexpr int kPer = NT / SPLIT;               // tokens that a CTA finishes
   constexpr int kG = kPer < 8 ? kPer : 8;        // of them at a time
+  constexpr int kHold = kPer < 64 ? kPer : 64;   // residuals held ahead
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -123,25 +124,25 @@ __global__ void __launch_bounds__(kThreads)
   const uint32_t tmem = *tmem_slot;
   const Ctx ctx{bars, abort_flag, p.status};
 
-  // This thread's feature and this CTA's tokens. The residual is fetched a group
-  // of tokens ahead, the first group while the products run; addresses past the
-  // end are clamped into the operand, so no load waits on a branch.
+  // This thread's feature and this CTA's tokens. The residual is fetched while the
+  // products run (64 tokens of it at most); addresses past the end are clamped
+  // into the operand, so no load waits on a branch.
   const int f = f0 + static_cast<int>(threadIdx.x);
   const bool f_on = f < p.N;
   const int fc = f_on ? f : p.N - 1;
   const int first = t0 + rank * kPer;
   const int end = p.M - first < kPer ? p.M : first + kPer;
   const uint16_t *res = OUT8 ? nullptr : static_cast<const uint16_t *>(p.residual.data);
-  uint16_t held[kG];
+  uint16_t held[kHold];
   auto fetch = [&](int tok) {
 #pragma unroll
-    for (int j = 0; j < kG; ++j) {
+    for (int j = 0; j < kHold; ++j) {
       const int t = tok + j < p.M ? tok + j : p.M - 1;
       held[j] = res[static_cast<int64_t>(t) * p.residual.ld + fc];
     }
   };
 #pragma unroll
-  for (int j = 0; j < kG; ++j) held[j] = 0;
+  for (int j = 0; j < kHold; ++j) held[j] = 0;
   if (res) fetch(first);
   const float bias = p.bias ? __ldg(p.bias + fc) : 0.f;
 
@@ -233,57 +234,61 @@ __global__ void __launch_bounds__(kThreads)
   }
   const float *part = reinterpret_cast<const float *>(smem + S::kOffPart) + threadIdx.x;
 #pragma unroll 1
-  for (int c = 0; c < kPer && first + c < end; c += kG) {
-    float v[kG];
-    if constexpr (SPLIT == 1) {
-      uint32_t d[8];
-      tmem_ld8(tcol + c, d);
-      tmem_ld_wait();
-      WF_REG_FENCE8(d, 0);
+  for (int base = 0; base < kPer; base += kHold) {
+    if (base > 0 && res) fetch(first + base);
 #pragma unroll
-      for (int j = 0; j < kG; ++j) v[j] = __uint_as_float(d[j]) + bias;
-    } else {
+    for (int h = 0; h < kHold; h += kG) {
+      const int c = base + h;
+      if (first + c >= end || !ok) break;
+      float v[kG];
+      if constexpr (SPLIT == 1) {
+        uint32_t d[8];
+        tmem_ld8(tcol + c, d);
+        tmem_ld_wait();
+        WF_REG_FENCE8(d, 0);
 #pragma unroll
-      for (int j = 0; j < kG; ++j) v[j] = part[(c + j) * 128];
+        for (int j = 0; j < kG; ++j) v[j] = __uint_as_float(d[j]) + bias;
+      } else {
 #pragma unroll
-      for (int r = 1; r < SPLIT; ++r)
+        for (int j = 0; j < kG; ++j) v[j] = part[(c + j) * 128];
 #pragma unroll
-        for (int j = 0; j < kG; ++j) v[j] += part[(r * kPer + c + j) * 128];
+        for (int r = 1; r < SPLIT; ++r)
 #pragma unroll
-      for (int j = 0; j < kG; ++j) v[j] += bias;
-    }
-    if (p.act == kGelu) {
+          for (int j = 0; j < kG; ++j) v[j] += part[(r * kPer + c + j) * 128];
 #pragma unroll
-      for (int j = 0; j < kG; ++j) v[j] = activate(v[j], kGelu);
-    } else if (p.act == kSilu) {
-#pragma unroll
-      for (int j = 0; j < kG; ++j) v[j] = activate(v[j], kSilu);
-    }
-    if constexpr (!OUT8) {
-      if (res) {
-#pragma unroll
-        for (int j = 0; j < kG; ++j) v[j] += __uint_as_float(static_cast<uint32_t>(held[j]) << 16);
-        if (kPer > kG) fetch(first + c + kG);
+        for (int j = 0; j < kG; ++j) v[j] += bias;
       }
-    }
-    if (!ok) continue;
+      if (p.act == kGelu) {
 #pragma unroll
-    for (int j = 0; j < kG; ++j) {
-      const int tok = first + c + j;
-      if constexpr (OUT8) {
-        // N is a multiple of 32: a warp's features are all inside or all outside.
-        const float a = fabsf(v[j]);
-        const uint32_t m = __reduce_max_sync(0xffffffffu, a == a ? __float_as_uint(a) : 0u);
-        const int ex = block_exponent(__uint_as_float(m));
-        if (f_on && tok < end) {
-          static_cast<uint8_t *>(p.out.data)[static_cast<int64_t>(tok) * p.out.ld + f] =
-              static_cast<uint8_t>(pack_e4m3x2(v[j] * block_factor(ex), 0.f) & 0xffu);
-          if (lane == 0)
-            p.out.scales[scale_offset(tok, f >> 5, g.out_block_tiles)] = static_cast<uint8_t>(ex + 127);
+        for (int j = 0; j < kG; ++j) v[j] = activate(v[j], kGelu);
+      } else if (p.act == kSilu) {
+#pragma unroll
+        for (int j = 0; j < kG; ++j) v[j] = activate(v[j], kSilu);
+      }
+      if constexpr (!OUT8) {
+        if (res) {
+#pragma unroll
+          for (int j = 0; j < kG; ++j) v[j] += __uint_as_float(static_cast<uint32_t>(held[h + j]) << 16);
         }
-      } else if (f_on && tok < end) {
-        static_cast<__nv_bfloat16 *>(p.out.data)[static_cast<int64_t>(tok) * p.out.ld + f] =
-            __float2bfloat16_rn(v[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < kG; ++j) {
+        const int tok = first + c + j;
+        if constexpr (OUT8) {
+          // N is a multiple of 32: a warp's features are all inside or all outside.
+          const float a = fabsf(v[j]);
+          const uint32_t m = __reduce_max_sync(0xffffffffu, a == a ? __float_as_uint(a) : 0u);
+          const int ex = block_exponent(__uint_as_float(m));
+          if (f_on && tok < end) {
+            static_cast<uint8_t *>(p.out.data)[static_cast<int64_t>(tok) * p.out.ld + f] =
+                static_cast<uint8_t>(pack_e4m3x2(v[j] * block_factor(ex), 0.f) & 0xffu);
+            if (lane == 0)
+              p.out.scales[scale_offset(tok, f >> 5, g.out_block_tiles)] = static_cast<uint8_t>(ex + 127);
+          }
+        } else if (f_on && tok < end) {
+          static_cast<__nv_bfloat16 *>(p.out.data)[static_cast<int64_t>(tok) * p.out.ld + f] =
+              __float2bfloat16_rn(v[j]);
+        }
       }
     }
   }

@@ -141,7 +141,7 @@ struct Plan {
   int bn, nt, split;
 };
 
-Plan plan_linear(const LinearParams &p, bool e4m3, bool out8) {
+Plan plan_linear(const LinearParams &p, bool e4m3, bool out8, bool direct) {
   const int64_t n_kb = (static_cast<int64_t>(p.K) + (e4m3 ? 127 : 63)) / (e4m3 ? 128 : 64);
   const auto tiles = [](int64_t n, int64_t by) { return (n + by - 1) / by; };
   Plan best{false, 0, 0, 0};
@@ -162,7 +162,8 @@ Plan plan_linear(const LinearParams &p, bool e4m3, bool out8) {
     const int64_t pairs = p.sms / 2, all = tiles(p.M, 256) * tiles(p.N, bn);
     const double k_block = (e4m3 ? (bn == 192 ? 0.376 : 0.70) : bn == 192 ? 0.38 : bn == 256 ? 0.45 : 0.66) *
                            (all <= pairs ? 0.72 : 1.0);
-    const double rest = e4m3 ? (bn == 192 ? 1.3 : 3.6) : bn == 192 ? 0.6 : bn == 256 ? 0.8 : 3.2;
+    const double rest = (e4m3 ? (bn == 192 ? 1.3 : 3.6) : bn == 192 ? 0.6 : bn == 256 ? 0.8 : 3.2) +
+                        (direct ? 1.5 : 0.0);
     offer(6.0 + tiles(all, pairs) * (n_kb * k_block + rest), Plan{true, bn, 0, 0});
   }
   // Features on the M side: either the chain of k-blocks of a CTA (two CTAs per SM
@@ -177,12 +178,14 @@ Plan plan_linear(const LinearParams &p, bool e4m3, bool out8) {
     const int64_t room = static_cast<int64_t>(p.sms) * (nt <= 64 ? 2 : 1);
     for (int split = 1; split <= 8 && split <= n_kb; split *= 2) {
       const double chain = static_cast<double>(tiles(n_kb, split)) * k_block + 0.05 * nt / split;
-      double us = tiles(all * split, room) * chain;
+      const int64_t waves = tiles(all * split, room);
+      double us = waves * chain;
       const double l2 = static_cast<double>(all) * n_kb * (16.0 + nt / 8.0) / 11e3;
       const double hbm = p.N * 128e-3 * n_kb / 6.5e3;
       us = us > l2 ? us : l2;
       us = us > hbm ? us : hbm;
-      offer(4.0 + us + (split == 8 ? 0.5 : 0.0), Plan{false, 0, nt, split});
+      // What does not overlap: a share of the chain, a start per further wave.
+      offer(4.0 + us + 0.25 * waves * chain + 1.5 * (waves - 1), Plan{false, 0, nt, split});
     }
     if (p.M <= nt) break;
   }
@@ -283,7 +286,7 @@ wf_status wf_linear(const wf_rows *x, const wf_rows *w, const float *bias, int32
   p.sms = dev.sms;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool stored_by_tma = rows16(out) && (!residual || rows16(residual));
-  const Plan plan = plan_linear(p, e4m3, out8);
+  const Plan plan = plan_linear(p, e4m3, out8, !stored_by_tma);
   return status_of(plan.pair ? launch_linear_pair(p, e4m3, out8, !stored_by_tma, plan.bn, st)
                              : launch_linear_skinny(p, e4m3, out8, plan.nt, plan.split, st));
 }
