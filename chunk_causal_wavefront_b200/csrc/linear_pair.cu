@@ -155,6 +155,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MX, BN, HALVES
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const Ctx ctx{bars, abort_flag, p.status};
+  grid_wait();
+  grid_trigger();
 
   if (warp == S::kProducerWarp) {
     // ------------------------------------------------------------ producer --
@@ -558,8 +560,8 @@ cudaError_t run_pair(const LinearParams &p, cudaStream_t st) {
   const cudaError_t e = allow_shared(linear_pair_kernel<MX, BN, HALVES, OUT8, DIRECT>, allowed, p.device, S::kSmemBytes);
   if (e != cudaSuccess) return e;
   const int pairs = g.total < p.sms / 2 ? g.total : p.sms / 2;
-  linear_pair_kernel<MX, BN, HALVES, OUT8, DIRECT><<<2 * pairs, S::kThreads, S::kSmemBytes, st>>>(p, g, tx, tw, tsx, tsw, tr, to);
-  return cudaGetLastError();
+  return launch_dependent(linear_pair_kernel<MX, BN, HALVES, OUT8, DIRECT>, 2 * pairs, S::kThreads, S::kSmemBytes, 0, st,
+                          p, g, tx, tw, tsx, tsw, tr, to);
 }
 
 }  // namespace

@@ -110,8 +110,10 @@ __global__ void __launch_bounds__(kThreads)
       *abort_flag = 0;
       for (int b = 0; b < S::kNumBars; ++b) mbar_init(bars + b, 1);
       fence_barrier_init();
-      for (int s = 0; s < filled; ++s) load(kb0 + s, s);
     }
+    grid_wait();
+    if (elect_one())
+      for (int s = 0; s < filled; ++s) load(kb0 + s, s);
     __syncwarp();
   } else if (warp == 1) {
     tmem_alloc(tmem_slot, S::kTmemCols);
@@ -123,6 +125,8 @@ __global__ void __launch_bounds__(kThreads)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const Ctx ctx{bars, abort_flag, p.status};
+  grid_wait();
+  grid_trigger();
 
   // This thread's feature and this CTA's tokens. The residual is fetched while the
   // products run (64 tokens of it at most); addresses past the end are clamped
@@ -334,18 +338,8 @@ cudaError_t run_skinny(const LinearParams &p, cudaStream_t st) {
   static std::atomic<uint64_t> allowed;
   const cudaError_t e = allow_shared(linear_skinny_kernel<MX, NT, SPLIT, OUT8>, allowed, p.device, S::kSmemBytes);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(ft * tt * SPLIT));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = S::kSmemBytes;
-  cfg.stream = st;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = SPLIT;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, linear_skinny_kernel<MX, NT, SPLIT, OUT8>, p, g, tx, tw, tsx, tsw);
+  return launch_dependent(linear_skinny_kernel<MX, NT, SPLIT, OUT8>, static_cast<unsigned>(ft * tt * SPLIT), kThreads,
+                          S::kSmemBytes, SPLIT, st, p, g, tx, tw, tsx, tsw);
 }
 
 template <bool MX, int NT, bool OUT8>

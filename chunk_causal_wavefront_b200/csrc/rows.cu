@@ -127,6 +127,8 @@ __global__ void __launch_bounds__(kNormThreads, (sizeof(T) == 2 ? 2 : 1) + (CH <
   };
   const int64_t step = static_cast<int64_t>(gridDim.x) * rows;
   int64_t base = static_cast<int64_t>(blockIdx.x) * rows;
+  sm100::grid_wait();
+  sm100::grid_trigger();
   load(base + sub);
   for (int turn = 0; base < p.rows; base += step, turn ^= 1) {
     const int64_t row = base + sub;
@@ -208,6 +210,8 @@ __global__ void __launch_bounds__(kAnyThreads) norm_any_kernel(const NormParams 
   const double inv = 1.0 / p.cols;
   const int block_tiles = (p.cols + 127) >> 7;
   int turn = 0;
+  sm100::grid_wait();
+  sm100::grid_trigger();
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
     const T *x = static_cast<const T *>(p.x.data) + row * p.x.ld;
     const T *r = p.residual.data ? static_cast<const T *>(p.residual.data) + row * p.residual.ld : nullptr;
@@ -282,6 +286,8 @@ __global__ void __launch_bounds__(256) quantize_kernel(const ConvertParams p) {
   const uint32_t per_row = static_cast<uint32_t>(p.cols) >> 4;
   const uint32_t total = static_cast<uint32_t>(p.rows) * per_row;   // even, < 2^31 (host check)
   const int block_tiles = (p.cols + 127) >> 7;
+  sm100::grid_wait();
+  sm100::grid_trigger();
   for (uint32_t i = blockIdx.x * 256u + threadIdx.x; i < total; i += gridDim.x * 256u) {
     const uint32_t row = i / per_row, k = i - row * per_row;
     const T *x = static_cast<const T *>(p.x.data) + static_cast<int64_t>(row) * p.x.ld + 16 * k;
@@ -319,6 +325,8 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const ConvertParams p) 
   const uint32_t per_row = static_cast<uint32_t>(p.cols) >> 4;
   const uint32_t total = static_cast<uint32_t>(p.rows) * per_row;
   const int block_tiles = (p.cols + 127) >> 7;
+  sm100::grid_wait();
+  sm100::grid_trigger();
   for (uint32_t i = blockIdx.x * 256u + threadIdx.x; i < total; i += gridDim.x * 256u) {
     const uint32_t row = i / per_row, k = i - row * per_row;
     const uint4 c = *reinterpret_cast<const uint4 *>(
@@ -375,8 +383,8 @@ cudaError_t run_norm(const NormParams &p, int wpr, const DeviceFacts &dev, cudaS
   const cudaError_t e = resident_blocks(norm_kernel<T, OUT8, CH>, threads, known[wpr], dev, &grid);
   if (e != cudaSuccess) return e;
   const int64_t need = (static_cast<int64_t>(p.rows) + rows - 1) / rows;
-  norm_kernel<T, OUT8, CH><<<static_cast<unsigned>(need < grid ? need : grid), threads, 0, st>>>(p, wpr);
-  return cudaGetLastError();
+  return launch_dependent(norm_kernel<T, OUT8, CH>, static_cast<unsigned>(need < grid ? need : grid), threads, 0, 0,
+                          st, p, wpr);
 }
 
 template <typename T, bool OUT8>
@@ -393,9 +401,9 @@ cudaError_t pick_norm(const NormParams &p, cudaStream_t st) {
   if (!vec) {
     const int64_t most = static_cast<int64_t>(dev.sms) * 16;
     const unsigned grid = static_cast<unsigned>(p.rows < most ? p.rows : most);
-    if (p.cols <= kAnyThreads * kAnyKeep) norm_any_kernel<T, OUT8, true><<<grid, kAnyThreads, 0, st>>>(p);
-    else norm_any_kernel<T, OUT8, false><<<grid, kAnyThreads, 0, st>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(p.cols <= kAnyThreads * kAnyKeep ? norm_any_kernel<T, OUT8, true>
+                                                             : norm_any_kernel<T, OUT8, false>,
+                            grid, kAnyThreads, 0, 0, st, p);
   }
   // Warps per row and chunks per lane that leave the fewest lanes idle; among
   // those the most chunks, for more bytes in flight per lane.
@@ -462,14 +470,12 @@ cudaError_t launch_quantize_rows(const ConvertParams &p, RowsType in, cudaStream
   const cudaError_t e = device_facts(&dev);
   if (e != cudaSuccess) return e;
   const unsigned grid = convert_grid(p, dev.sms);
-  if (in == RowsType::kBf16) {
-    if (aligned(p.x.data, p.x.ld, 2)) quantize_kernel<__nv_bfloat16, true><<<grid, 256, 0, st>>>(p);
-    else quantize_kernel<__nv_bfloat16, false><<<grid, 256, 0, st>>>(p);
-  } else {
-    if (aligned(p.x.data, p.x.ld, 4)) quantize_kernel<float, true><<<grid, 256, 0, st>>>(p);
-    else quantize_kernel<float, false><<<grid, 256, 0, st>>>(p);
-  }
-  return cudaGetLastError();
+  if (in == RowsType::kBf16)
+    return launch_dependent(aligned(p.x.data, p.x.ld, 2) ? quantize_kernel<__nv_bfloat16, true>
+                                                         : quantize_kernel<__nv_bfloat16, false>,
+                            grid, 256, 0, 0, st, p);
+  return launch_dependent(aligned(p.x.data, p.x.ld, 4) ? quantize_kernel<float, true> : quantize_kernel<float, false>,
+                          grid, 256, 0, 0, st, p);
 }
 
 cudaError_t launch_dequantize_rows(const ConvertParams &p, RowsType out, cudaStream_t st) {
@@ -477,14 +483,13 @@ cudaError_t launch_dequantize_rows(const ConvertParams &p, RowsType out, cudaStr
   const cudaError_t e = device_facts(&dev);
   if (e != cudaSuccess) return e;
   const unsigned grid = convert_grid(p, dev.sms);
-  if (out == RowsType::kBf16) {
-    if (aligned(p.out.data, p.out.ld, 2)) dequantize_kernel<__nv_bfloat16, true><<<grid, 256, 0, st>>>(p);
-    else dequantize_kernel<__nv_bfloat16, false><<<grid, 256, 0, st>>>(p);
-  } else {
-    if (aligned(p.out.data, p.out.ld, 4)) dequantize_kernel<float, true><<<grid, 256, 0, st>>>(p);
-    else dequantize_kernel<float, false><<<grid, 256, 0, st>>>(p);
-  }
-  return cudaGetLastError();
+  if (out == RowsType::kBf16)
+    return launch_dependent(aligned(p.out.data, p.out.ld, 2) ? dequantize_kernel<__nv_bfloat16, true>
+                                                             : dequantize_kernel<__nv_bfloat16, false>,
+                            grid, 256, 0, 0, st, p);
+  return launch_dependent(aligned(p.out.data, p.out.ld, 4) ? dequantize_kernel<float, true>
+                                                           : dequantize_kernel<float, false>,
+                          grid, 256, 0, 0, st, p);
 }
 
 }  // namespace wf

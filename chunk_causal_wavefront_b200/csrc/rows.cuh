@@ -11,6 +11,8 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include <utility>
+
 #include "wf.h"
 
 namespace wf {
@@ -42,6 +44,29 @@ struct LinearParams {
   int32_t *status;                  // the device's row-operator status word
   int32_t device, sms;
 };
+
+// A launch that may start while the one before it in the stream is leaving (its
+// kernel calls grid_wait before it touches global memory), in clusters of `cluster`
+// blocks (0: the kernel's own, or none). Calls back to back: 1 x 6144 x 1536 linear
+// 6.5 -> 5.3 us, 23400 x 1536 norm 51.4 -> 49.8 us.
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned threads, uint32_t shared,
+                             unsigned cluster, cudaStream_t st, A &&...args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = shared;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
 
 enum class RowsType { kBf16, kF32, kE4m3 };
 

@@ -372,6 +372,14 @@ __device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float
   return r;
 }
 
+// Programmatic dependent launch. grid_wait: the launch before this one in the stream
+// has completed and its memory is visible; nothing global may be read or written
+// before it. grid_trigger: the next launch may start its blocks as this one's leave.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_trigger() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // One lane of a converged warp: nonzero in the elected lane.
 __device__ __forceinline__ uint32_t elect_one() {
   uint32_t r;
