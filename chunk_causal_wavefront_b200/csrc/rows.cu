@@ -12,8 +12,8 @@
 //   warps share a row, each lane holds up to four chunks of 8 elements (16-byte
 //   loads of bf16), and the next row's loads are issued before this row's sum is
 //   reduced. The weight comes from L1 (held in registers it cost occupancy). The
-//   sum of squares is fp32: per lane, then by shuffles, then over the row's warps
-//   through shared memory in a fixed order.
+//   sum of squares is fp32 per lane and 64 bits from there: by shuffles, then over
+//   the row's warps through shared memory in a fixed order.
 //   E4M3 output: a block of 32 columns is four neighbouring lanes' chunks, so its
 //   largest magnitude takes two shuffles; the codes are made from the fp32
 //   values, not from their bf16 rounding.
@@ -78,16 +78,27 @@ __device__ __forceinline__ float widen(float v) { return v; }
 __device__ __forceinline__ void narrow(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void narrow(float *p, float v) { *p = v; }
 
-__device__ __forceinline__ float warp_sum(float v) {
+__device__ __forceinline__ double warp_sum(double v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
-// 1 / sqrt(mean + eps), once per row in 64 bits and rounded once: a row's elements
-// share this factor's error, which could carry many of them over an E4M3 rounding.
-__device__ __forceinline__ float norm_scale(float ss, double inv_cols, float eps) {
-  return static_cast<float>(rsqrt(static_cast<double>(ss) * inv_cols + static_cast<double>(eps)));
+// 1 / sqrt(mean + eps), computed in 64 bits and rounded once: a row's elements
+// share this factor's error.
+__device__ __forceinline__ float norm_factor(double ss, double inv_cols, float eps) {
+  return static_cast<float>(rsqrt(ss * inv_cols + static_cast<double>(eps)));
+}
+// s * factor * w rounded to fp32: twice on the way to bf16 or fp32, once (factor *
+// w as a sum of two floats) on the way to E4M3, where every error carries a few
+// values over the border between two codes.
+template <bool ONCE>
+__device__ __forceinline__ float scaled(float s, float factor, float w) {
+  if constexpr (!ONCE) return s * factor * w;
+  const float c = factor * w;
+  // fmaxf drops the NaN that an infinite product's remainder is.
+  const float rest = fmaxf(fmaf(factor, w, -c), -1e30f);
+  return fmaf(s, c, s * rest);
 }
 
 // Largest magnitude; fmaxf leaves NaN out.
@@ -104,7 +115,7 @@ __device__ __forceinline__ float amax8(const float (&v)[8]) {
 // inputs: a chunk is stored by the thread that loaded it, and rows do not overlap.
 template <typename T, bool OUT8, int CH>
 __global__ void __launch_bounds__(kNormThreads, (sizeof(T) == 2 ? 2 : 1) + (CH < 4)) norm_kernel(const NormParams p, const int wpr) {
-  __shared__ float part[2][kNormThreads / 32];
+  __shared__ double part[2][kNormThreads / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = warp / wpr;                      // row of the block's pass
   const int rows = blockDim.x / 32 / wpr;
@@ -150,15 +161,15 @@ __global__ void __launch_bounds__(kNormThreads, (sizeof(T) == 2 ? 2 : 1) + (CH <
       }
     }
     load(row + step);
-    ss = warp_sum(ss);
+    double sum = warp_sum(static_cast<double>(ss));
     if (wpr > 1) {
       // Two sets of partial sums in turn, so one barrier per pass is enough.
-      if (lane == 0) part[turn][warp] = ss;
+      if (lane == 0) part[turn][warp] = sum;
       __syncthreads();
-      ss = 0.f;
-      for (int i = 0; i < wpr; ++i) ss += part[turn][sub * wpr + i];
+      sum = 0.0;
+      for (int i = 0; i < wpr; ++i) sum += part[turn][sub * wpr + i];
     }
-    const float scale = norm_scale(ss, inv, p.eps);
+    const float factor = norm_factor(sum, inv, p.eps);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int k = t + c * stride;
@@ -174,7 +185,7 @@ __global__ void __launch_bounds__(kNormThreads, (sizeof(T) == 2 ? 2 : 1) + (CH <
         w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[c][i] = v[c][i] * scale * w[i];
+      for (int i = 0; i < 8; ++i) v[c][i] = scaled<OUT8>(v[c][i], factor, w[i]);
       if constexpr (OUT8) {
         float m = amax8(v[c]);
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
@@ -205,7 +216,7 @@ constexpr int kAnyKeep = 16;
 
 template <typename T, bool OUT8, bool KEEP>
 __global__ void __launch_bounds__(kAnyThreads) norm_any_kernel(const NormParams p) {
-  __shared__ float part[2][kAnyThreads / 32];
+  __shared__ double part[2][kAnyThreads / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const double inv = 1.0 / p.cols;
   const int block_tiles = (p.cols + 127) >> 7;
@@ -243,16 +254,16 @@ __global__ void __launch_bounds__(kAnyThreads) norm_any_kernel(const NormParams 
         ss = fmaf(v, v, ss);
       }
     }
-    ss = warp_sum(ss);
-    if (lane == 0) part[turn][warp] = ss;
+    double sum = warp_sum(static_cast<double>(ss));
+    if (lane == 0) part[turn][warp] = sum;
     __syncthreads();
-    ss = 0.f;
+    sum = 0.0;
 #pragma unroll
-    for (int i = 0; i < kAnyThreads / 32; ++i) ss += part[turn][i];
-    const float scale = norm_scale(ss, inv, p.eps);
+    for (int i = 0; i < kAnyThreads / 32; ++i) sum += part[turn][i];
+    const float factor = norm_factor(sum, inv, p.eps);
     // cols is a multiple of 32 for E4M3, so a warp is wholly in or out there.
     auto finish = [&](int64_t k, float s) {
-      const float v = s * scale * (p.weight ? __ldg(p.weight + k) : 1.0f);
+      const float v = scaled<OUT8>(s, factor, p.weight ? __ldg(p.weight + k) : 1.0f);
       if (p.sum.data) narrow(static_cast<T *>(p.sum.data) + row * p.sum.ld + k, s);
       if constexpr (OUT8) {
         const float a = fabsf(v);
