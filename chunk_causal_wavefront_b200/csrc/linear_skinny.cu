@@ -22,7 +22,7 @@
 //   Measured (captured graph, weights in HBM): 1 x 6144 x 1536 bf16 6.8 us (18.9 MB;
 //   the weights alone 2.9 us at 6.55 TB/s, the rest is the latency of launch, first
 //   loads, cluster barriers and last stores), 24 x 5120 x 5120 E4M3 9.5 us, 64 x 1536
-//   x 1536 bf16 5.9 us, 1111 x 1000 x 1544 14.5 us (against 15 on CTA pairs).
+//   x 1536 bf16 5.9 us, 1111 x 1000 x 1544 13.7 us (against 14.6 on CTA pairs).
 // Every wait is bounded; a timeout is recorded in the row-operator status word.
 #include <cuda.h>
 #include <cuda_bf16.h>

@@ -3,9 +3,9 @@
 //
 // All three read each element once and write each result once; HBM bounds them.
 // Measured, of the 6554 GB/s that a copy reaches: norm with residual, 23400 x 1536
-// bf16 48.5 us (90 %), 23400 x 5120 to E4M3 139 us (93 %); without residual 27.4 us
-// (80 %: half the bytes in flight per row); 23400 x 5120 bf16 to E4M3 60 us (92 %)
-// and back 62 us (90 %); a single row 2.7 us, all of it launch and latency.
+// bf16 48.0 us (91 %), 23400 x 5120 to E4M3 143 us (90 %); without residual 27.7 us
+// (79 %: half the bytes in flight per row); 23400 x 5120 bf16 to E4M3 58 us (95 %)
+// and back 60 us (92 %); a single row 2.7 us, all of it launch and latency.
 //
 // Norm: s = x + residual, out = s / sqrt(mean(s^2) + eps) * weight.
 //   A row stays in registers between its one read and its one write: up to 8
