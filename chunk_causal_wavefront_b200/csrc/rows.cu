@@ -17,8 +17,10 @@
 //   E4M3 output: a block of 32 columns is four neighbouring lanes' chunks, so its
 //   largest magnitude takes two shuffles; the codes are made from the fp32
 //   values, not from their bf16 rounding.
-//   Rows that 16-byte loads cannot take (odd widths or strides) or that are too
-//   wide (over 8192 columns) go through a block per row, element by element.
+//   Rows of odd width go through a like kernel on the aligned chunks that they
+//   cover; rows that are too wide (over 8192 columns), or that start at different
+//   places within 16 bytes in different operands, through a block per row, element
+//   by element.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -82,6 +84,17 @@ __device__ __forceinline__ double warp_sum(double v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
+}
+
+__device__ __forceinline__ Raw16 pack8(const __nv_bfloat16 (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = __bfloat16_as_ushort(v[2 * i]) | static_cast<uint32_t>(__bfloat16_as_ushort(v[2 * i + 1])) << 16;
+  return {make_uint4(w[0], w[1], w[2], w[3])};
+}
+__device__ __forceinline__ Raw32 pack8(const float (&v)[8]) {
+  return {make_float4(v[0], v[1], v[2], v[3]), make_float4(v[4], v[5], v[6], v[7])};
 }
 
 // 1 / sqrt(mean + eps), computed in 64 bits and rounded once: a row's elements
@@ -203,6 +216,131 @@ __global__ void __launch_bounds__(kNormThreads, (sizeof(T) == 2 ? 2 : 1) + (CH <
       } else if (on) {
         store8(static_cast<T *>(p.out.data) + row * p.out.ld + 8 * k, v[c]);
       }
+    }
+  }
+}
+
+// The same for rows that start anywhere within 16 bytes (odd widths), at the same
+// place in every operand. Chunks are those of memory: chunk k of a row holds its
+// elements [8 k - mis, 8 k - mis + 8), mis the elements between the aligned address
+// and the row's start. A chunk that reaches into the neighbouring rows is loaded whole
+// (the strange elements are dropped) unless it leaves the operand, and stored
+// element by element. The weight is staged in shared memory: at eight loads of it per
+// chunk that no vector load can replace, and a select for each, this bounds the kernel:
+// 23400 x 1001 bf16 37 us, with residual 48 (60 % of HBM; element by element 53 and
+// 70), 23400 x 5119 159 and 190 us (193 and 352).
+template <typename T, int CH>
+__global__ void __launch_bounds__(kNormThreads, (sizeof(T) == 2 ? 2 : 1) + (CH < 4)) norm_shift_kernel(const NormParams p, const int wpr) {
+  __shared__ double part[2][kNormThreads / 32];
+  extern __shared__ float weight[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sub = warp / wpr;                      // row of the block's pass
+  const int rows = blockDim.x / 32 / wpr;
+  const int t = (warp - sub * wpr) * 32 + lane;    // thread of the row
+  const int stride = 32 * wpr;
+  const double inv = 1.0 / p.cols;
+  const T *x = static_cast<const T *>(p.x.data), *r = static_cast<const T *>(p.residual.data);
+  typename RawOf<T>::type rx[CH] = {}, rr[CH] = {};
+  auto shift_of = [&](int64_t row) {
+    return static_cast<int>((reinterpret_cast<uintptr_t>(x + row * p.x.ld) & 15u) / sizeof(T));
+  };
+  // Element of the row that chunk c of this thread starts at.
+  auto start_of = [&](int c, int mis) { return 8 * (t + c * stride) - mis; };
+  auto whole = [&](int e) { return e >= 0 && e + 8 <= p.cols; };
+  auto fetch = [&](const T *row_data, int64_t row, int e, typename RawOf<T>::type &raw) {
+    if (whole(e) || ((e >= 0 || row > 0) && (e + 8 <= p.cols || row + 1 < p.rows))) {
+      raw = load8(row_data + e);
+    } else {
+      T part[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        narrow(part + i, 0.f);
+        if (e + i >= 0 && e + i < p.cols) part[i] = row_data[e + i];
+      }
+      raw = pack8(part);
+    }
+  };
+  auto load = [&](int64_t row) {
+    if (row >= p.rows) return;
+    const int mis = shift_of(row);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int e = start_of(c, mis);
+      if (e < p.cols) {
+        fetch(x + row * p.x.ld, row, e, rx[c]);
+        if (r) fetch(r + row * p.residual.ld, row, e, rr[c]);
+      }
+    }
+  };
+  const int64_t step = static_cast<int64_t>(gridDim.x) * rows;
+  int64_t base = static_cast<int64_t>(blockIdx.x) * rows;
+  sm100::grid_wait();
+  sm100::grid_trigger();
+  for (int i = threadIdx.x; i < p.cols; i += blockDim.x) weight[i + (i >> 3)] = p.weight ? p.weight[i] : 1.0f;
+  __syncthreads();
+  load(base + sub);
+  for (int turn = 0; base < p.rows; base += step, turn ^= 1) {
+    const int64_t row = base + sub;
+    const bool live = row < p.rows;
+    const int mis = shift_of(row);
+    float v[CH][8];
+    float ss = 0.f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      widen8(rx[c], v[c]);
+      if (r) {
+        float u[8];
+        widen8(rr[c], u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[c][i] += u[i];
+      }
+      const int e = start_of(c, mis);
+      if (!whole(e)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (e + i < 0 || e + i >= p.cols) v[c][i] = 0.f;
+      }
+      if (e < p.cols) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss = fmaf(v[c][i], v[c][i], ss);
+      }
+    }
+    load(row + step);
+    double sum = warp_sum(static_cast<double>(ss));
+    if (wpr > 1) {
+      // Two sets of partial sums in turn, so one barrier per pass is enough.
+      if (lane == 0) part[turn][warp] = sum;
+      __syncthreads();
+      sum = 0.0;
+      for (int i = 0; i < wpr; ++i) sum += part[turn][sub * wpr + i];
+    }
+    const float factor = norm_factor(sum, inv, p.eps);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int e = start_of(c, mis);
+      const bool on = live && e < p.cols;
+      auto store = [&](T *row_data) {
+        if (whole(e)) {
+          store8(row_data + e, v[c]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (e + i >= 0 && e + i < p.cols) narrow(row_data + e + i, v[c][i]);
+        }
+      };
+      if (on && p.sum.data) store(static_cast<T *>(p.sum.data) + row * p.sum.ld);
+      // Element x of the weight is at x + x / 8 in shared memory, so that lanes 8
+      // elements apart do not meet in one bank.
+      const float *w = weight + 9 * (t + c * stride) - mis;
+      if (whole(e)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[c][i] = scaled<false>(v[c][i], factor, w[i - (i < mis)]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (e + i >= 0 && e + i < p.cols) v[c][i] = scaled<false>(v[c][i], factor, w[i - (i < mis)]);
+      }
+      if (on) store(static_cast<T *>(p.out.data) + row * p.out.ld);
     }
   }
 }
@@ -385,17 +523,47 @@ cudaError_t resident_blocks(K kernel, int threads, std::atomic<int> (&known)[64]
   return cudaSuccess;
 }
 
-template <typename T, bool OUT8, int CH>
-cudaError_t run_norm(const NormParams &p, int wpr, const DeviceFacts &dev, cudaStream_t st) {
-  static std::atomic<int> known[9][64];
+// One launch of norm_kernel or norm_shift_kernel with `shared` dynamic bytes.
+template <typename K>
+cudaError_t run_norm(K kernel, std::atomic<int> (&known)[9][64], const NormParams &p, int wpr, uint32_t shared,
+                     const DeviceFacts &dev, cudaStream_t st) {
   const int rows = kNormThreads / 32 / wpr;        // per block and pass, >= 1
   const int threads = rows * wpr * 32;
   int64_t grid = 0;
-  const cudaError_t e = resident_blocks(norm_kernel<T, OUT8, CH>, threads, known[wpr], dev, &grid);
+  const cudaError_t e = resident_blocks(kernel, threads, known[wpr], dev, &grid);
   if (e != cudaSuccess) return e;
   const int64_t need = (static_cast<int64_t>(p.rows) + rows - 1) / rows;
-  return launch_dependent(norm_kernel<T, OUT8, CH>, static_cast<unsigned>(need < grid ? need : grid), threads, 0, 0,
-                          st, p, wpr);
+  return launch_dependent(kernel, static_cast<unsigned>(need < grid ? need : grid), threads, shared, 0, st, p, wpr);
+}
+
+template <typename T, bool OUT8, int CH, bool SHIFT>
+cudaError_t run_chunks(const NormParams &p, int wpr, const DeviceFacts &dev, cudaStream_t st) {
+  static std::atomic<int> known[9][64];
+  if constexpr (SHIFT)
+    return run_norm(norm_shift_kernel<T, CH>, known, p, wpr, (p.cols + p.cols / 8 + 1) * 4, dev, st);
+  else
+    return run_norm(norm_kernel<T, OUT8, CH>, known, p, wpr, 0, dev, st);
+}
+
+template <typename T, bool OUT8, bool SHIFT>
+cudaError_t pick_chunks(const NormParams &p, const DeviceFacts &dev, cudaStream_t st) {
+  // Warps per row and chunks per lane that leave the fewest lanes idle; among
+  // those the most chunks, for more bytes in flight per lane.
+  const int chunks = (p.cols + (SHIFT ? 7 + 15 / static_cast<int>(sizeof(T)) : 0)) / 8;
+  int wpr = 8, ch = 4;
+  for (int c = 4; c >= 1; --c) {
+    const int w = (chunks + 32 * c - 1) / (32 * c);
+    if (w <= 8 && w * c < wpr * ch) {
+      wpr = w;
+      ch = c;
+    }
+  }
+  switch (ch) {
+    case 1: return run_chunks<T, OUT8, 1, SHIFT>(p, wpr, dev, st);
+    case 2: return run_chunks<T, OUT8, 2, SHIFT>(p, wpr, dev, st);
+    case 3: return run_chunks<T, OUT8, 3, SHIFT>(p, wpr, dev, st);
+    default: return run_chunks<T, OUT8, 4, SHIFT>(p, wpr, dev, st);
+  }
 }
 
 template <typename T, bool OUT8>
@@ -409,30 +577,21 @@ cudaError_t pick_norm(const NormParams &p, cudaStream_t st) {
                    (!p.sum.data || aligned(p.sum.data, p.sum.ld, elt)) &&
                    aligned(p.out.data, p.out.ld, OUT8 ? 1 : elt) &&
                    (reinterpret_cast<uintptr_t>(p.weight) & 15u) == 0;
-  if (!vec) {
-    const int64_t most = static_cast<int64_t>(dev.sms) * 16;
-    const unsigned grid = static_cast<unsigned>(p.rows < most ? p.rows : most);
-    return launch_dependent(p.cols <= kAnyThreads * kAnyKeep ? norm_any_kernel<T, OUT8, true>
-                                                             : norm_any_kernel<T, OUT8, false>,
-                            grid, kAnyThreads, 0, 0, st, p);
+  if (vec) return pick_chunks<T, OUT8, false>(p, dev, st);
+  if constexpr (!OUT8) {
+    // Every operand's rows start at the same place within 16 bytes.
+    const auto like_x = [&](const RowsView &o) {
+      return !o.data || ((reinterpret_cast<uintptr_t>(o.data) - reinterpret_cast<uintptr_t>(p.x.data)) % 16 == 0 &&
+                         (p.rows == 1 || (o.ld - p.x.ld) * elt % 16 == 0));
+    };
+    if (p.cols >= 64 && p.cols <= 8192 - 16 && like_x(p.residual) && like_x(p.sum) && like_x(p.out))
+      return pick_chunks<T, false, true>(p, dev, st);
   }
-  // Warps per row and chunks per lane that leave the fewest lanes idle; among
-  // those the most chunks, for more bytes in flight per lane.
-  const int chunks = p.cols / 8;
-  int wpr = 8, ch = 4;
-  for (int c = 4; c >= 1; --c) {
-    const int w = (chunks + 32 * c - 1) / (32 * c);
-    if (w <= 8 && w * c < wpr * ch) {
-      wpr = w;
-      ch = c;
-    }
-  }
-  switch (ch) {
-    case 1: return run_norm<T, OUT8, 1>(p, wpr, dev, st);
-    case 2: return run_norm<T, OUT8, 2>(p, wpr, dev, st);
-    case 3: return run_norm<T, OUT8, 3>(p, wpr, dev, st);
-    default: return run_norm<T, OUT8, 4>(p, wpr, dev, st);
-  }
+  const int64_t most = static_cast<int64_t>(dev.sms) * 16;
+  const unsigned grid = static_cast<unsigned>(p.rows < most ? p.rows : most);
+  return launch_dependent(p.cols <= kAnyThreads * kAnyKeep ? norm_any_kernel<T, OUT8, true>
+                                                           : norm_any_kernel<T, OUT8, false>,
+                          grid, kAnyThreads, 0, 0, st, p);
 }
 
 unsigned convert_grid(const ConvertParams &p, int sms) {

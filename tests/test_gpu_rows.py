@@ -132,6 +132,38 @@ def test_norm_strided(ld, offset):
     assert (np.abs(f64(out) - want) <= np.abs(want) * (HALF[BF16] + 80 * 2.0 ** -24) * 1.01).all()
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("cols,ld,offset,n", [(65, 65, 1, 40), (250, 250, 5, 3), (1001, 1001, 0, 57), (1001, 1004, 3, 57),
+                                              (1001, 1009, 7, 1), (4099, 4107, 2, 9), (8171, 8171, 1, 2), (2049, 2049, 0, 600)])
+def test_norm_rows_at_any_place(cols, ld, offset, n, dtype):
+    """Rows that start anywhere, with NaN before, between and behind them that must neither leak in
+    nor change, in and out of place."""
+    def buffer(seed):
+        flat = torch.full((offset + n * ld + 16,), float("nan"), dtype=dtype, device="cuda")
+        v = flat[offset:offset + n * ld].view(n, ld)[:, :cols]
+        v.copy_(rows(n, cols, seed, dtype))
+        return flat, v
+
+    def gaps(flat):
+        f = flat.clone()
+        f[offset:offset + n * ld].view(n, ld)[:, :cols] = 0
+        return f
+
+    (fx, x), (fr, r), (fo, o), (fs, s) = (buffer(i) for i in range(120, 124))
+    w = vec(cols, 124, 1.0)
+    want, _ = R.add_rms_norm(f64(x), f64(r), f64(w), 1e-6)
+    total = (x.float() + r.float()).to(dtype)
+    tol = np.abs(want) * (HALF[dtype] + (cols / 32 + 24) * 2.0 ** -24) * 1.01
+    wfb.add_rms_norm(x, w, residual=r, out=o, sum_out=s)
+    assert torch.equal(s, total) and (np.abs(f64(o) - want) <= tol).all()
+    kept = o.clone()
+    wfb.add_rms_norm(x, w, residual=r, out=x, sum_out=r)
+    assert torch.equal(r, total) and torch.equal(x, kept)
+    for flat in (fx, fr, fo, fs):
+        g = gaps(flat)
+        assert torch.equal(g.isnan(), gaps(torch.full_like(flat, float("nan"))).isnan())
+
+
 @pytest.mark.parametrize("cols", [1536, 1001, 8200])
 def test_norm_in_place(cols):
     x0, r0, w = rows(300, cols, 15), rows(300, cols, 16), vec(cols, 17, 1.0)
