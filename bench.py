@@ -18,6 +18,9 @@ The default run also measures, in the same process, the 14B-shaped layer, the
 "other_workloads"), times the float64 oracle on the host cores
 ("cpu_baseline") and the same step from pinned host buffers ("e2e").
 
+--layer bf16|e4m3 times whole transformer layers instead (norms, projections,
+attention and feed-forward with dummy weights) and prints its own line.
+
 Usage: python bench.py [--gpus N] [--steps K] [--warmup W] [--impl ours|reference]
 With --gpus N > 1 and no torchrun environment, the script relaunches itself as
 N ranks (one process per GPU) under torch.distributed.run.
