@@ -72,12 +72,35 @@ class LayerRound:
         return r[:self.pool.live_rows] if slot is None else r[slot * chunk:(slot + 1) * chunk]
 
     def _check(self, h: torch.Tensor, w: LayerWeights) -> Optional[str]:
+        """Everything that a layer reads, before its first call: the pool's calls take addresses
+        without shapes, and a refusal half-way would leave h between two states."""
         if h.dtype != torch.bfloat16 or h.numel() != self.q_rot.numel() or not h.is_contiguous():
             raise ValueError("h must be a contiguous bf16 tensor [S+1][C][hidden]")
         kinds = {isinstance(m, E4M3Rows) for m in (w.w_qkv, w.w_out, w.w_up, w.w_down)}
         if len(kinds) != 1:
             raise ValueError("weights must be all bf16 or all E4M3 rows")
-        return "e4m3" if kinds.pop() else None
+        e4m3 = kinds.pop()
+        hidden, ffn = self.hidden, w.w_up.shape[0]
+        given = [("h", h)]
+        for name, shape in (("w_qkv", (3 * hidden, hidden)), ("w_out", (hidden, hidden)),
+                            ("w_up", (ffn, hidden)), ("w_down", (hidden, ffn))):
+            m = getattr(w, name)
+            if tuple(m.shape) != shape or not (e4m3 or m.dtype == torch.bfloat16):
+                raise ValueError(f"{name} must be {list(shape)} in bf16 or E4M3 rows, not {list(m.shape)}")
+            given.append((name, m))
+        for name, n in (("norm1", hidden), ("norm2", hidden), ("b_out", hidden), ("b_up", ffn), ("b_down", hidden)):
+            v = getattr(w, name)
+            if v is None:
+                continue
+            if v.dtype != torch.float32 or v.shape != (n,) or not v.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous float32 vector of {n} elements")
+            given.append((name, v))
+        for name, t in given:
+            if t.device != self.q_rot.device:
+                raise ValueError(f"{name} is on {t.device}, the pool on {self.q_rot.device}")
+            if t.requires_grad and torch.is_grad_enabled():
+                raise ValueError("layers compute no gradients: call them under torch.no_grad()")
+        return "e4m3" if e4m3 else None
 
     # -- the two halves around the K/V exchange -------------------------------------------
     def _publish(self, layer: int, h: torch.Tensor, w: LayerWeights, slot: Optional[int]) -> None:
