@@ -347,8 +347,10 @@ __global__ void __launch_bounds__(kNormThreads, (sizeof(T) == 2 ? 2 : 1) + (CH <
 
 // Any width, alignment and stride: one block per row, element by element. Up to
 // 2048 columns the row stays in registers (KEEP), all its loads in flight at once;
-// longer rows are read twice. A thread's elements are the same in both readings,
-// so outputs may be the inputs.
+// longer rows are read twice, a thread's squares summed in fp32 sixteen at a time and
+// in 64 bits from there (a row may have 2^24 columns per thread, and an fp32 sum
+// stands still at that many). A thread's elements are the same in both readings, so
+// outputs may be the inputs.
 constexpr int kAnyThreads = 128;
 constexpr int kAnyKeep = 16;
 
@@ -366,6 +368,7 @@ __global__ void __launch_bounds__(kAnyThreads) norm_any_kernel(const NormParams 
     const T *r = p.residual.data ? static_cast<const T *>(p.residual.data) + row * p.residual.ld : nullptr;
     float held[KEEP ? kAnyKeep : 1];
     float ss = 0.f;
+    double sum = 0.0;
     if constexpr (KEEP) {
       T a[kAnyKeep], b[kAnyKeep];
 #pragma unroll
@@ -387,12 +390,23 @@ __global__ void __launch_bounds__(kAnyThreads) norm_any_kernel(const NormParams 
         ss = fmaf(held[j], held[j], ss);
       }
     } else {
-      for (int64_t k = threadIdx.x; k < p.cols; k += kAnyThreads) {
+      int64_t k = threadIdx.x;
+      for (; k + (kAnyKeep - 1) * kAnyThreads < p.cols; k += kAnyKeep * kAnyThreads) {
+        ss = 0.f;
+#pragma unroll
+        for (int j = 0; j < kAnyKeep; ++j) {
+          const float v = widen(x[k + j * kAnyThreads]) + (r ? widen(r[k + j * kAnyThreads]) : 0.f);
+          ss = fmaf(v, v, ss);
+        }
+        sum += static_cast<double>(ss);
+      }
+      ss = 0.f;
+      for (; k < p.cols; k += kAnyThreads) {
         const float v = widen(x[k]) + (r ? widen(r[k]) : 0.f);
         ss = fmaf(v, v, ss);
       }
     }
-    double sum = warp_sum(static_cast<double>(ss));
+    sum = warp_sum(sum + static_cast<double>(ss));
     if (lane == 0) part[turn][warp] = sum;
     __syncthreads();
     sum = 0.0;
