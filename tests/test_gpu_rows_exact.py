@@ -45,3 +45,35 @@ def test_norm_error_does_not_grow_with_the_width(cols, terms, residual):
     # (one rounding), so the bound is relative everywhere.
     off = np.abs(f64(out) - want)
     assert (off <= np.abs(want) * (terms / 2 + 5) * 2.0 ** -24 * 1.01).all(), float((off / np.abs(want)).max() * 2 ** 24)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("cols", [96, 1536, 8224])
+def test_norm_to_e4m3_near_the_ends_of_fp32(cols, dtype):
+    """Rows near zero, so that the row's factor times a large weight is past fp32's range where the
+    result is not, with weights of both signs, and infinite weights. The result is as any other: half
+    a step of E4M3 (2^-4 of the value; the block's smallest step is 2^-10 of its scale), and before
+    that the fp32 error of this file's bound."""
+    n = 40
+    g = np.random.default_rng([2, cols])
+    x = torch.from_numpy(2.0 ** -14 * g.choice([-1.0, 1.0, 0.5], (n, cols))).to(dtype).cuda()
+    w = g.uniform(0.5, 1.0, cols) * 1e37 * np.where(np.arange(cols) % 3 == 0, -1, 1)
+    w[:32] = np.where(np.arange(32) % 2, np.inf, -np.inf)             # the first block: infinities alone
+    w = torch.from_numpy(w).float().cuda()
+    q = wfb.add_rms_norm(x, w, eps=1e-6, out_dtype="e4m3")
+    want, _ = R.add_rms_norm(f64(x), None, f64(w), 1e-6)
+    assert (np.abs(want[:, 32:]).max() < 2.0 ** 127) and (np.abs(f64(w)[32:]) * 900 > 2.0 ** 128).any()
+    got = f64(q.dequantize(dtype=F32))
+    np.testing.assert_array_equal(got[:, :32], want[:, :32])          # infinite, with the sign
+    _, e = R.quantize(want)
+    tol = np.maximum(np.abs(want) * (2.0 ** -4 + 2.0 ** -18), np.repeat(2.0 ** (e - 10.0), 32, axis=1))[:, 32:]
+    assert (np.abs(got[:, 32:] - want[:, 32:]) <= tol).all()
+
+
+def test_norm_to_e4m3_without_eps_near_zero():
+    """eps = 0: the factor is as large as the row is small, whatever the weight."""
+    x = torch.full((3, 64), 2.0 ** -60, device="cuda")
+    w = torch.full((64,), 2.0 ** 70, device="cuda")
+    w[::2] = -w[::2]
+    got = f64(wfb.add_rms_norm(x, w, eps=0.0, out_dtype="e4m3").dequantize(dtype=F32))
+    np.testing.assert_array_equal(got, np.broadcast_to(f64(w), (3, 64)))
