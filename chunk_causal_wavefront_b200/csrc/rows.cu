@@ -406,12 +406,16 @@ __global__ void __launch_bounds__(kAnyThreads) norm_any_kernel(const NormParams 
     } else {
       int64_t k = threadIdx.x;
       for (; k + (kAnyKeep - 1) * kAnyThreads < p.cols; k += kAnyKeep * kAnyThreads) {
+        float v[kAnyKeep];                             // loads in flight together
+#pragma unroll
+        for (int j = 0; j < kAnyKeep; ++j) v[j] = widen(x[k + j * kAnyThreads]);
+        if (r) {
+#pragma unroll
+          for (int j = 0; j < kAnyKeep; ++j) v[j] += widen(r[k + j * kAnyThreads]);
+        }
         ss = 0.f;
 #pragma unroll
-        for (int j = 0; j < kAnyKeep; ++j) {
-          const float v = widen(x[k + j * kAnyThreads]) + (r ? widen(r[k + j * kAnyThreads]) : 0.f);
-          ss = fmaf(v, v, ss);
-        }
+        for (int j = 0; j < kAnyKeep; ++j) ss = fmaf(v[j], v[j], ss);
         sum += static_cast<double>(ss);
       }
       ss = 0.f;
