@@ -77,3 +77,49 @@ def test_norm_to_e4m3_without_eps_near_zero():
     w[::2] = -w[::2]
     got = f64(wfb.add_rms_norm(x, w, eps=0.0, out_dtype="e4m3").dequantize(dtype=F32))
     np.testing.assert_array_equal(got, np.broadcast_to(f64(w), (3, 64)))
+
+
+def factor_of(x, eps=0.0):
+    """The rows' factor: computed in 64 bits from the exact sum, rounded once. (The kernel's 64-bit
+    reciprocal root may be an ulp of 64 bits away, which changes the fp32 rounding of one row in 2^27.)"""
+    s = x.astype(np.float64)
+    return (1 / np.sqrt((s * s).sum(1, keepdims=True) * (1.0 / x.shape[1]) + eps)).astype(np.float32)
+
+
+@pytest.mark.parametrize("cols", [63, 1001, 1536, 8192, 20479])
+def test_norm_sums_meet_in_64_bits(cols):
+    """Whole numbers whose squares a thread adds without rounding (32 x 700^2 < 2^24), while a row's sum
+    needs more than 24 bits: with every later sum in 64 bits, out is s * factor, bit for bit."""
+    n = 200
+    x = np.random.default_rng([3, cols]).integers(-700, 701, (n, cols)).astype(np.float32)
+    x[:, 0] = 1
+    out = wfb.add_rms_norm(torch.from_numpy(x).cuda(), eps=0.0)
+    np.testing.assert_array_equal(out.cpu().numpy(), x * factor_of(x))
+
+
+@pytest.mark.parametrize("cols,shift,dtype", [(96, 0, F32), (96, 0, BF16), (1536, 0, BF16), (96, 1, F32), (8224, 0, BF16)])
+def test_norm_rounds_once_before_e4m3(cols, shift, dtype):
+    """Values beside the borders between codes, where a rounding more ends on the other side.
+    s has 4 bits and factor and weight 24 each, so s * factor * weight is exact in float64; one rounding
+    to fp32 must give the codes."""
+    n = 16
+    g = np.random.default_rng([4, cols, shift])
+    s = g.integers(1, 16, cols).astype(np.float64)
+    x = (s * g.choice([-1.0, 1.0], (n, cols))).astype(np.float32)    # one factor for all rows
+    f = factor_of(x)
+    assert (f == f[0]).all()
+    f = f.astype(np.float64)
+    # Midpoints of two codes from 2^-2 to 2^8, and a block's largest value, 448.
+    mid = (1 + (2 * g.integers(0, 7, cols) + 1) / 16) * 2.0 ** g.integers(-2, 8, cols)
+    mid[::32] = 448
+    w = (mid / (s * f[0, 0])).astype(np.float32)
+    w = np.nextafter(w, w * (1 + g.integers(-1, 2, cols) * 1.0).astype(np.float32))
+    w[::32] = (448 / (s * f[0, 0]))[::32] * 0.99
+    t = torch.zeros(n, cols + shift, device="cuda")[:, shift:]
+    t.copy_(torch.from_numpy(x))
+    q = wfb.add_rms_norm(t.to(dtype) if dtype is BF16 else t, torch.from_numpy(w).cuda(), eps=0.0, out_dtype="e4m3")
+    codes, e = R.quantize((x.astype(np.float64) * f * w.astype(np.float64)).astype(np.float32))
+    twice, _ = R.quantize((x * f.astype(np.float32)) * w)
+    assert (codes != twice).mean() > 0.02                     # these inputs do tell
+    np.testing.assert_array_equal(q.codes.view(torch.uint8).cpu().numpy(), codes)
+    np.testing.assert_array_equal(R.untile_scales(q.scales.cpu().numpy(), n, cols // 32), e)
