@@ -249,4 +249,12 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_rows_bind", nullptr, -1, g_meth
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__rows_bind() { return PyModule_Create(&g_module); }
+PyMODINIT_FUNC PyInit__rows_bind() {
+  PyObject *m = PyModule_Create(&g_module);
+  // The torch whose headers this was built with; the package compares it with the one it runs under.
+  if (m && PyModule_AddStringConstant(m, "torch_version", WF_TORCH_VERSION) != 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

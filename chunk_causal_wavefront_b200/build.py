@@ -10,6 +10,7 @@ import argparse
 import concurrent.futures as cf
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -23,7 +24,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libwf.so")
 
 BIND_SRC = os.path.join(PKG, "bind", "rows_bind.cpp")
-BIND = os.path.join(PKG, "_rows_bind.so")
+# Its name carries the interpreter's ABI, so that no other Python tries to load it.
+BIND = os.path.join(PKG, "_rows_bind" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O3", "-I", INCLUDE, "-I", CSRC]
@@ -62,18 +64,32 @@ def _compile(src: str, verbose: bool, extra) -> str:
     return obj
 
 
+def torch_version(torch_dir: str) -> str:
+    """__version__ of the torch in this directory, without importing it."""
+    with open(os.path.join(torch_dir, "version.py")) as f:
+        return re.search(r"^__version__ = '([^']+)'", f.read(), re.M).group(1)
+
+
 def build_bind(force: bool = False, verbose: bool = False) -> str:
     """The compiled common case of the row operators' torch-facing calls, against the installed
-    torch's headers (found without importing it)."""
+    torch's headers (found without importing it). It is rebuilt for another torch, whose version it
+    carries: the package loads it only under that one."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.origin:
+        raise RuntimeError("torch is not installed")
+    torch = os.path.dirname(spec.origin)
+    version = torch_version(torch)
+    stamp = os.path.join(BUILD, os.path.basename(BIND) + ".torch")
     deps = [BIND_SRC, os.path.join(INCLUDE, "wf.h")]
     if not force and os.path.exists(BIND) and os.path.getmtime(BIND) >= max(map(os.path.getmtime, deps)):
-        return BIND
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+        if os.path.exists(stamp) and open(stamp).read() == version:
+            return BIND
     cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
     system = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
               cuda, sysconfig.get_paths()["include"]]
     tmp = BIND + ".tmp"
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE]
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE,
+           f'-DWF_TORCH_VERSION="{version}"']
     for d in system:
         cmd += ["-isystem", d]
     cmd += [BIND_SRC, "-o", tmp, "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch",
@@ -84,7 +100,21 @@ def build_bind(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"building {BIND_SRC} failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BIND)
+    with open(stamp, "w") as f:
+        f.write(version)
     return BIND
+
+
+def try_build_bind(force: bool = False, verbose: bool = False) -> str | None:
+    """build_bind, or a report and no module: the library needs none, the row operators' calls only
+    take more of the host's time. What an earlier build left may not fit the library any more."""
+    try:
+        return build_bind(force, verbose)
+    except (RuntimeError, OSError, AttributeError) as e:
+        if os.path.exists(BIND):
+            os.remove(BIND)
+        print(f"warning: the row operators' compiled binding was not built: {e}", file=sys.stderr, flush=True)
+        return None
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
@@ -107,7 +137,7 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
-    build_bind(force, verbose)
+    try_build_bind(force, verbose)
     return LIB
 
 

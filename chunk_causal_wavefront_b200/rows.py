@@ -18,6 +18,7 @@ import importlib
 import importlib.util
 import math
 import struct
+import warnings
 from typing import Optional, Tuple, Union
 
 import torch
@@ -158,14 +159,32 @@ def _entry(name: str):
 _quantize, _dequantize = _entry("wf_quantize_rows"), _entry("wf_dequantize_rows")
 _norm, _linear = _entry("wf_add_rms_norm"), _entry("wf_linear")
 
-# The compiled common case (contiguous tensors on the current device, outputs to be
-# allocated, current stream): the same library calls with less of the host's time.
-# It answers NotImplemented where the code below has to check, refuse or convert;
-# without the built module that code serves every call.
-_fast = None
-if importlib.util.find_spec(__package__ + "._rows_bind") is not None:
-    _fast = importlib.import_module(__package__ + "._rows_bind")
-    _fast.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (_linear, _norm, _quantize, _dequantize)))
+def _load_fast():
+    """The compiled common case of the calls below, or None.
+
+    It is the same library calls with less of the host's time, for contiguous tensors on the current
+    device, outputs to be allocated and the current stream; it answers NotImplemented where the code
+    below has to check, refuse or convert. Without it that code serves every call, so a module that
+    was built for another torch, or does not load, is left alone."""
+    name = __package__ + "._rows_bind"
+    if importlib.util.find_spec(name) is None:
+        return None
+    try:
+        fast = importlib.import_module(name)
+        built = fast.torch_version
+    except (ImportError, OSError, SystemError, AttributeError) as e:
+        why = str(e)
+    else:
+        if built == str(torch.__version__):
+            fast.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (_linear, _norm, _quantize, _dequantize)))
+            return fast
+        why = f"it was built for torch {built}, this is {torch.__version__}"
+    warnings.warn(f"{name} is not used ({why}): small row operators take more host time until "
+                  "chunk_causal_wavefront_b200/build.py has run", RuntimeWarning, stacklevel=2)
+    return None
+
+
+_fast = _load_fast()
 
 
 def _made(codes: torch.Tensor, scales: torch.Tensor) -> "E4M3Rows":
