@@ -30,7 +30,8 @@ decltype(&wf_dequantize_rows) g_dequantize = nullptr;
 bool given(PyObject *o) { return o != Py_None; }
 
 // A contiguous strided tensor of at least one dimension on the current device, of
-// one of two types, that records no gradient. Clears *ok otherwise.
+// one of two types, that records no gradient and carries no tangent (and has memory
+// of its own: what a function transform wraps has none). Clears *ok otherwise.
 const Tensor &plain(PyObject *o, at::ScalarType a, at::ScalarType b, bool *ok) {
   static const Tensor none;
   if (!THPVariable_CheckExact(o)) {
@@ -39,10 +40,10 @@ const Tensor &plain(PyObject *o, at::ScalarType a, at::ScalarType b, bool *ok) {
   }
   const Tensor &t = THPVariable_Unpack(o);
   const auto type = t.scalar_type();
-  if (!t.is_cuda() || t.layout() != at::kStrided || (type != a && type != b) || t.dim() < 1 ||
+  if (!t.is_cuda() || t.layout() != at::kStrided || !t.has_storage() || (type != a && type != b) || t.dim() < 1 ||
       !t.is_contiguous() || t.is_conj() || t.is_neg() || t.size(-1) == 0 ||
       t.get_device() != c10::cuda::current_device() ||
-      (c10::GradMode::is_enabled() && t.requires_grad()))
+      (c10::GradMode::is_enabled() && t.requires_grad()) || t._fw_grad(/*level=*/0).defined())
     *ok = false;
   return t;
 }

@@ -21,7 +21,7 @@ import torch
 
 from . import wf as _wf
 from .pool import KVPool
-from .rows import E4M3Rows, add_rms_norm, linear, quantize_rows
+from .rows import E4M3Rows, add_rms_norm, linear, quantize_rows, refuse_gradients
 
 Weight = Union[torch.Tensor, E4M3Rows]
 
@@ -98,8 +98,7 @@ class LayerRound:
         for name, t in given:
             if t.device != self.q_rot.device:
                 raise ValueError(f"{name} is on {t.device}, the pool on {self.q_rot.device}")
-            if t.requires_grad and torch.is_grad_enabled():
-                raise ValueError("layers compute no gradients: call them under torch.no_grad()")
+        refuse_gradients("layers", *(t for _, t in given))
         return "e4m3" if e4m3 else None
 
     # -- the two halves around the K/V exchange -------------------------------------------

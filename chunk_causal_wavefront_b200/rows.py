@@ -8,7 +8,7 @@ libwf's kernels; PyTorch allocates outputs that the caller does not give.
 
 The calls enqueue on ``stream`` (default: the tensors' device's current stream)
 and do not synchronise. They compute no gradients and refuse tensors that want
-them while gradients are recorded.
+them while gradients are recorded, and tensors that carry a forward-mode tangent.
 """
 from __future__ import annotations
 
@@ -22,6 +22,7 @@ import warnings
 from typing import Optional, Tuple, Union
 
 import torch
+from torch.autograd.forward_ad import unpack_dual
 
 from . import wf as _wf
 from .wf import WfError
@@ -198,6 +199,21 @@ def _check(status: int, what: str) -> None:
         raise WfError(status, what)
 
 
+def refuse_gradients(what: str, *operands: Optional[Operand]) -> None:
+    """Raises if an operand wants a gradient that nothing here would compute: one that records, or a
+    dual tensor, whose tangent the result would lose (also under torch.no_grad())."""
+    recording = torch.is_grad_enabled()
+    for t in operands:
+        if t is None:
+            continue
+        if isinstance(t, E4M3Rows):
+            t = t.codes
+        if recording and t.requires_grad:
+            raise ValueError(f"{what} compute no gradients: call them under torch.no_grad()")
+        if unpack_dual(t).tangent is not None:
+            raise ValueError(f"{what} compute no tangents: give them the primal of a dual tensor")
+
+
 def _here(stream, x, *others) -> Optional[int]:
     """Checks that everything is on one CUDA device. The raw current stream if that device is
     current and no stream is given; else None: the call goes through _elsewhere."""
@@ -207,9 +223,7 @@ def _here(stream, x, *others) -> Optional[int]:
     for t in others:
         if t is not None and t.get_device() != index:
             raise ValueError(f"all tensors must be on one device: got {x.device} and {t.device}")
-    if torch.is_grad_enabled() and (x.requires_grad or any([t is not None and t.requires_grad
-                                                            for t in others])):
-        raise ValueError("row operators compute no gradients: call them under torch.no_grad()")
+    refuse_gradients("row operators", x, *others)
     if stream is not None:
         if stream.device != x.device:
             raise ValueError(f"the stream is on {stream.device}, the tensors on {x.device}")
