@@ -9,7 +9,7 @@
 // MMAs, every CTA receives the accumulator of its own 128 rows in its own TMEM, and
 // two accumulators take turns, so that one tile's epilogue runs under the next
 // tile's products. BN = 256 is for bf16 only (two accumulators fill TMEM); BN = 192
-// leaves 128 columns, which hold four stages of scales for E4M3.
+// leaves 128 columns, which hold every stage's scales for E4M3.
 //   What bounds it is not the tensor pipe but the operands' way from L2 (without
 // loads 4680 x 20480 x 5120 bf16 takes 501 us at 1965 MHz, with them 640, and the
 // number of stages changes nothing). So a tile may have two halves of BN = 192
@@ -104,7 +104,7 @@ struct Shape {
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
   static_assert(!MX || 2 * BN <= kScaleCols, "TMEM");
   static_assert(HALVES == 1 || 2 * kStages <= kWideMinBlocks, "k-blocks of a wide tile");
-  static_assert(!MX || 4 * 4 * (1 + kScaleTiles) <= 512 - kScaleCols, "TMEM");
+  static_assert(!MX || kStages * 4 * (1 + kScaleTiles) <= 512 - kScaleCols, "TMEM");
 };
 
 struct PairGrid {
@@ -228,7 +228,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MX, BN, HALVES
         const uint32_t b_lo = a_lo + (kABytes >> 4);
         const int left = g.k_steps - kb * (S::kKElems / S::kKStep);
         if (elect_one()) {
-          const uint32_t sfa = tmem + kScaleCols + 4 * (1 + S::kScaleTiles) * (qq & 3);
+          // A stage's scales have their own columns: the stage is refilled only after its
+          // products have completed, and no rule orders a copy behind earlier products.
+          const uint32_t sfa = tmem + kScaleCols + 4 * (1 + S::kScaleTiles) * s;
           const uint32_t sfb = sfa + 4;
           if (MX && first) {
             const uint32_t sc = sc0 + s * S::kScaleBytes;

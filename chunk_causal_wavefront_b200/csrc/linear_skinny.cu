@@ -54,10 +54,10 @@ struct Shape {
   static constexpr int kFull0 = 0, kEmpty0 = kStages, kAcc = 2 * kStages, kNumBars = 2 * kStages + 1;
   static constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;
   static constexpr uint32_t kSmemBytes = kOffMisc + 16 + 1024;   // + alignment slack
-  // D, then four stages of scales (4 columns of w, 4 of x each).
+  // D, then every stage's scales (4 columns of w, 4 of x each).
   static constexpr uint32_t kTmemCols = !MX ? (NT < 32 ? 32 : NT) : (NT <= 32 ? 64 : 2 * NT);
   static_assert(kOperandBytes % 1024 == 0, "alignment");
-  static_assert(!MX || NT + 32 <= static_cast<int>(kTmemCols), "TMEM");
+  static_assert(!MX || NT + 8 * kStages <= static_cast<int>(kTmemCols), "TMEM");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
 
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kThreads)
       if (elect_one()) {
         if constexpr (MX) {
           const uint32_t sc = sc0 + s * S::kScaleBytes;
-          const uint32_t sfa = tmem + NT + 8 * (q & 3);
+          const uint32_t sfa = tmem + NT + 8 * s;         // a stage's own columns
           const uint32_t sfb = sfa + 4;
           tmem_copy_scales(sfa, make_desc_scale_tile(sc));
           tmem_copy_scales(sfb, make_desc_scale_tile(sc + 512));

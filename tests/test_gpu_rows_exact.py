@@ -123,3 +123,27 @@ def test_norm_rounds_once_before_e4m3(cols, shift, dtype):
     assert (codes != twice).mean() > 0.02                     # these inputs do tell
     np.testing.assert_array_equal(q.codes.view(torch.uint8).cpu().numpy(), codes)
     np.testing.assert_array_equal(R.untile_scales(q.scales.cpu().numpy(), n, cols // 32), e)
+
+
+@pytest.mark.parametrize("n,features,blocks", [(1, 512, 40), (20, 1000, 24), (120, 1000, 40), (600, 1000, 40),
+                                               (4600, 1528, 24)])
+def test_linear_with_other_scales_in_every_block(n, features, blocks):
+    """Block scales that change by up to 2^12 from one step along K to the next, over many rounds of the
+    stages: a scale of another step would show. Products and scales are exact in fp32; K of them
+    are added with an error of (K / 16 + 16) 2^-23 of S = sum |x| |w| (the unit may truncate), and one
+    rounding to bf16 follows."""
+    K = 128 * blocks
+    g = np.random.default_rng([5, n, features])
+
+    def operand(rows):
+        v = g.standard_normal((rows, K)) * np.repeat(2.0 ** g.integers(-6, 7, (rows, K // 32)), 32, axis=1)
+        codes, e = R.quantize(v)
+        return (wfb.E4M3Rows(torch.from_numpy(codes).cuda().view(torch.float8_e4m3fn),
+                             torch.from_numpy(R.tile_scales(e, fill=255)).cuda()), R.dequantize(codes, e))
+
+    (x, xv), (w, wv) = operand(n), operand(features)
+    want, S = xv @ wv.T, np.abs(xv) @ np.abs(wv).T
+    for _ in range(3):
+        got = f64(wfb.linear(x, w))
+        assert (np.abs(got - want) <= np.abs(want) * 2.0 ** -8 + (K / 16 + 16) * 2.0 ** -23 * S * (1 + 2.0 ** -8)).all()
+    assert wfb.rows_check_status() == 0
