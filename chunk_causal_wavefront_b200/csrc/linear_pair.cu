@@ -154,7 +154,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MX, BN, HALVES
   cluster_sync();                           // barriers of both CTAs initialised, TMEM allocated
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const Ctx ctx{bars, abort_flag, p.status};
+  const Ctx ctx{bars, abort_flag, p.status, p.wait_limit};
   grid_wait();
   grid_trigger();
 
@@ -171,7 +171,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MX, BN, HALVES
         const int s = q % S::kStages;
         ok = __all_sync(0xffffffffu, wait_bar(ctx, S::kEmpty0 + s, ((q / S::kStages) & 1) ^ 1));
         if (!ok) break;
-        if (elect_one()) {
+        const bool skip = kb == p.skip_k_block && t == pair && rank == 0;   // test hook
+        if (!skip && elect_one()) {
           // The leader expects the bytes of both CTAs on its full barrier.
           if (rank == 0) mbar_arrive_expect_tx(bars + S::kFull0 + s, 2 * S::kStageBytes);
           uint8_t *sa = smem + s * S::kOperandBytes;

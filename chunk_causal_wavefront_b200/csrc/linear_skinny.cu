@@ -93,6 +93,7 @@ __global__ void __launch_bounds__(kThreads)
   // The producer warp initialises the barriers and fills the empty ring before
   // anyone else is ready, so the first bytes are under way during the set-up.
   auto load = [&](int kb, int s) {
+    if (kb == p.skip_k_block) return;
     uint64_t *full = bars + S::kFull0 + s;
     mbar_arrive_expect_tx(full, S::kStageBytes);
     uint8_t *sa = smem + s * S::kOperandBytes;
@@ -124,7 +125,7 @@ __global__ void __launch_bounds__(kThreads)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const Ctx ctx{bars, abort_flag, p.status};
+  const Ctx ctx{bars, abort_flag, p.status, p.wait_limit};
   grid_wait();
   grid_trigger();
 

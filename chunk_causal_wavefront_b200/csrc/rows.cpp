@@ -192,6 +192,28 @@ Plan plan_linear(const LinearParams &p, bool e4m3, bool out8, bool direct) {
   return best;
 }
 
+// Whether this product has an instance of the kernel and tile.
+bool offers(const Plan &plan, const LinearParams &p, bool e4m3, bool out8) {
+  const int64_t n_kb = (static_cast<int64_t>(p.K) + (e4m3 ? 127 : 63)) / (e4m3 ? 128 : 64);
+  if (plan.pair)
+    return plan.bn == 192 || (plan.bn == 256 && !e4m3 && !out8) || (plan.bn == 384 && n_kb >= kWideMinBlocks);
+  const int nt = plan.nt, split = plan.split;
+  if ((nt != 16 && nt != 32 && nt != 64 && nt != 128) || (split != 1 && split != 2 && split != 4 && split != 8))
+    return false;
+  return split <= n_kb && (!e4m3 || nt >= 64 || p.M <= nt);
+}
+
+// Test hook, consumed by the thread's next product.
+struct NextLinear {
+  bool armed = false, forced = false;
+  Plan plan{};
+  int32_t skip_k_block = -1;
+  long long wait_limit = 0;
+};
+thread_local NextLinear t_next;
+
+constexpr long long kWaitLimit = 2000000000LL;   // ~1 s at 2 GHz
+
 bool rows16(const wf_rows *r) {
   return multiple_of(r->data, 16) && row_stride(r) * element_size(r->dtype) % 16 == 0;
 }
@@ -286,9 +308,33 @@ wf_status wf_linear(const wf_rows *x, const wf_rows *w, const float *bias, int32
   p.sms = dev.sms;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool stored_by_tma = rows16(out) && (!residual || rows16(residual));
-  const Plan plan = plan_linear(p, e4m3, out8, !stored_by_tma);
+  p.skip_k_block = -1;
+  p.wait_limit = kWaitLimit;
+  const NextLinear next = t_next;
+  t_next = NextLinear{};
+  if (next.armed) {
+    p.skip_k_block = next.skip_k_block;
+    p.wait_limit = next.wait_limit;
+    if (next.forced && !offers(next.plan, p, e4m3, out8)) return WF_ERR_INVALID_ARG;
+  }
+  const Plan plan = next.forced ? next.plan : plan_linear(p, e4m3, out8, !stored_by_tma);
   return status_of(plan.pair ? launch_linear_pair(p, e4m3, out8, !stored_by_tma, plan.bn, st)
                              : launch_linear_skinny(p, e4m3, out8, plan.nt, plan.split, st));
+}
+
+wf_status wf_rows_debug_next_linear(int32_t kernel, int32_t tile, int32_t split, int32_t skip_k_block,
+                                    int64_t wait_limit_cycles) {
+  if (kernel < 0 || kernel > 2 || skip_k_block < -1 || wait_limit_cycles < 1000 || wait_limit_cycles > kWaitLimit)
+    return WF_ERR_INVALID_ARG;
+  if (kernel == 1 && tile != 16 && tile != 32 && tile != 64 && tile != 128) return WF_ERR_INVALID_ARG;
+  if (kernel == 1 && split != 1 && split != 2 && split != 4 && split != 8) return WF_ERR_INVALID_ARG;
+  if (kernel == 2 && tile != 192 && tile != 256 && tile != 384) return WF_ERR_INVALID_ARG;
+  t_next.armed = true;
+  t_next.forced = kernel != 0;
+  t_next.plan = kernel == 2 ? Plan{true, tile, 0, 0} : Plan{false, 0, tile, split};
+  t_next.skip_k_block = skip_k_block;
+  t_next.wait_limit = wait_limit_cycles;
+  return WF_OK;
 }
 
 wf_status wf_rows_check_status(wf_stream_t stream) {

@@ -43,6 +43,10 @@ struct LinearParams {
   int32_t M, N, K;
   int32_t *status;                  // the device's row-operator status word
   int32_t device, sms;
+  // Test hook (wf_rows_debug_next_linear): a k-block that is not loaded (-1: none), and the
+  // cycles after which a wait gives up.
+  int32_t skip_k_block;
+  long long wait_limit;
 };
 
 // A launch that may start while the one before it in the stream is leaving (its

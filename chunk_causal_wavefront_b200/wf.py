@@ -41,7 +41,7 @@ EXPORTS = (
     "wf_project_publish", "wf_publish_kv_slot", "wf_round_attention_slot", "wf_deliver_kv",
     "wf_pool_debug_stall_next_attention", "wf_ipc_get_mem_handle", "wf_ipc_open_mem",
     "wf_ipc_close_mem", "wf_scale_bytes", "wf_quantize_rows", "wf_dequantize_rows",
-    "wf_add_rms_norm", "wf_linear", "wf_rows_check_status",
+    "wf_add_rms_norm", "wf_linear", "wf_rows_debug_next_linear", "wf_rows_check_status",
 )
 
 
@@ -123,6 +123,7 @@ def _load():
         "wf_dequantize_rows": (I32, [rowsp, rowsp, P]),
         "wf_add_rms_norm": (I32, [rowsp, rowsp, P, F32, rowsp, rowsp, P]),
         "wf_linear": (I32, [rowsp, rowsp, P, I32, rowsp, rowsp, P]),
+        "wf_rows_debug_next_linear": (I32, [I32, I32, I32, I32, I64]),
         "wf_rows_check_status": (I32, [P]),
     }
     for name, (res, args) in sig.items():
@@ -299,6 +300,11 @@ def wf_add_rms_norm(x: WfRows, residual: Optional[WfRows], weight: Optional[int]
 def wf_linear(x: WfRows, w: WfRows, bias: Optional[int], act: int, residual: Optional[WfRows],
               out: WfRows, stream: int) -> int:
     return _lib.wf_linear(x, w, bias, act, residual, out, stream or None)
+
+
+def wf_rows_debug_next_linear(kernel: int, tile: int = 0, split: int = 0, skip_k_block: int = -1,
+                              wait_limit_cycles: int = 2000000000) -> int:
+    return _lib.wf_rows_debug_next_linear(kernel, tile, split, skip_k_block, wait_limit_cycles)
 
 
 def wf_rows_check_status(stream: int) -> int:
