@@ -192,11 +192,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MX, BN, HALVES
       }
     }
     // Tail: every stage this CTA filled has been consumed by the MMAs, so no
-    // load of this CTA is in flight when it exits.
-    for (int s = 0; s < S::kStages && q > 0; ++s) {
+    // load of this CTA is in flight when it exits; if they gave up, it has landed.
+    ok = true;
+    for (int s = 0; ok && s < S::kStages; ++s) {
       const int fills = q / S::kStages + (s < q % S::kStages ? 1 : 0);
-      if (fills > 0) drain_wait(ctx, S::kEmpty0 + s, (fills - 1) & 1);
+      if (fills > 0) ok = __all_sync(0xffffffffu, wait_bar(ctx, S::kEmpty0 + s, (fills - 1) & 1));
     }
+    if (!ok) let_loads_land();
   } else if (warp == S::kMmaWarp) {
     // ---------------------------------------------------------- MMA issuer --
     if (rank == 0) {

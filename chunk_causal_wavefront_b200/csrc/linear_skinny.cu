@@ -160,11 +160,12 @@ __global__ void __launch_bounds__(kThreads)
       if (elect_one()) load(kb, s);
       __syncwarp();
     }
-    // Tail: every filled stage has been consumed, so no load is in flight when
-    // the CTA exits.
+    // Tail: every filled stage has been consumed or, if the products gave up, has
+    // landed, so no load is in flight when the CTA exits.
     for (int s = 0; s < S::kStages; ++s) {
       const int fills = q / S::kStages + (s < q % S::kStages ? 1 : 0);
-      if (fills > 0) drain_wait(ctx, S::kEmpty0 + s, (fills - 1) & 1);
+      if (fills == 0 || __all_sync(0xffffffffu, wait_bar(ctx, S::kEmpty0 + s, (fills - 1) & 1))) continue;
+      if (kb0 + s + (fills - 1) * S::kStages != p.skip_k_block) drain_wait(ctx, S::kFull0 + s, (fills - 1) & 1);
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer --

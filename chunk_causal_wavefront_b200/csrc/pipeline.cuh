@@ -23,6 +23,7 @@ namespace wf {
 
 constexpr long long kWaitLimit = 2000000000LL;   // ~1 s at 2 GHz (default per-launch limit)
 constexpr long long kDrainLimit = 4000000000LL;  // ~2 s: bound of the drain waits
+constexpr long long kLandCycles = 200000000LL;   // ~0.1 s: bound of let_loads_land
 
 struct Ctx {
   uint64_t *bars;
@@ -81,6 +82,13 @@ __device__ __forceinline__ bool drain_wait(const Ctx &c, int b, uint32_t parity)
     }
   }
   return true;
+}
+
+// For loads whose bytes count on the other CTA's barrier, which this one cannot watch:
+// once the pair has given up, time in which any TMA load lands.
+__device__ __forceinline__ void let_loads_land() {
+  const long long t0 = clock64();
+  while (clock64() - t0 < kLandCycles) __nanosleep(1000);
 }
 
 // Keep the compiler from using tcgen05.ld results before tcgen05.wait::ld.

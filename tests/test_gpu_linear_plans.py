@@ -1,6 +1,10 @@
-"""Every instance of the two product kernels, whatever wf_linear's estimate would choose, through
-wf_rows_debug_next_linear. Tolerances: check_linear's."""
+"""Every instance of the two product kernels, whatever wf_linear's estimate would choose, and their
+bounded waits, through wf_rows_debug_next_linear. Tolerances: check_linear's."""
+import time
+
 import pytest
+import torch
+
 from test_gpu_rows import check_linear, quantized, rows, vec
 
 import chunk_causal_wavefront_b200 as wfb
@@ -86,3 +90,30 @@ def test_products_without_an_instance_are_refused():
         wfb.linear(a, b, out_dtype=out)                                  # the hook is used up
     assert wfb.rows_check_status() == 0
 
+
+# A k-block that is never loaded: every wait behind it runs out after about a millisecond, the call
+# reports it, and the next call is as before. Early and late blocks, of the first and a later CTA of a
+# cluster; one tile and several per pair.
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("n,features,plan,block", [(5, 300, (FEW, 16, 1), 0), (60, 300, (FEW, 64, 4), 5),
+                                                   (128, 300, (FEW, 128, 8), 8), (200, 300, (FEW, 128, 1), 7),
+                                                   (130, 200, (PAIRS, 192), 0), (2590, 3000, (PAIRS, 192), 7),
+                                                   (2590, 3000, (PAIRS, 384), 6), (2590, 2999, (PAIRS, 384), 9)])
+def test_waits_run_out(n, features, plan, block, e4m3):
+    k = 128 * 10 if e4m3 else 64 * 10
+    x, w, _, _ = operands(n, features, k, e4m3, 230)
+    r = rows(n, features, 232)
+    force(*plan)
+    want = wfb.linear(x, w, residual=r)
+    torch.cuda.synchronize()
+    for _ in range(2):
+        force(*plan, skip_k_block=block, wait_limit_cycles=2000000)
+        t0 = time.monotonic()
+        wfb.linear(x, w, residual=r)
+        assert wfb.rows_check_status() == W.WF_ERR_TIMEOUT
+        assert time.monotonic() - t0 < 1.0
+        assert wfb.rows_check_status() == 0
+        force(*plan)
+        assert torch.equal(wfb.linear(x, w, residual=r), want)
+        assert torch.equal(wfb.linear(x, w), wfb.linear(x, w))
+    assert wfb.rows_check_status() == 0
