@@ -171,8 +171,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MX, BN, HALVES
         const int s = q % S::kStages;
         ok = __all_sync(0xffffffffu, wait_bar(ctx, S::kEmpty0 + s, ((q / S::kStages) & 1) ^ 1));
         if (!ok) break;
-        const bool skip = kb == p.skip_k_block && t == pair && rank == 0;   // test hook
-        if (!skip && elect_one()) {
+        // Test hook: the products stall, since the leader's bytes do not come.
+        const bool stall = kb == p.stall_k_block && rank == 0;
+        if (!stall && elect_one()) {
           // The leader expects the bytes of both CTAs on its full barrier.
           if (rank == 0) mbar_arrive_expect_tx(bars + S::kFull0 + s, 2 * S::kStageBytes);
           uint8_t *sa = smem + s * S::kOperandBytes;
@@ -192,13 +193,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MX, BN, HALVES
       }
     }
     // Tail: every stage this CTA filled has been consumed by the MMAs, so no
-    // load of this CTA is in flight when it exits; if they gave up, it has landed.
-    ok = true;
-    for (int s = 0; ok && s < S::kStages; ++s) {
+    // load of this CTA is in flight when it exits; or they have had time to land.
+    for (int s = 0; s < S::kStages && q > 0; ++s) {
       const int fills = q / S::kStages + (s < q % S::kStages ? 1 : 0);
-      if (fills > 0) ok = __all_sync(0xffffffffu, wait_bar(ctx, S::kEmpty0 + s, (fills - 1) & 1));
+      if (fills > 0) drain_wait(ctx, S::kEmpty0 + s, (fills - 1) & 1, kTailLimit);
     }
-    if (!ok) let_loads_land();
   } else if (warp == S::kMmaWarp) {
     // ---------------------------------------------------------- MMA issuer --
     if (rank == 0) {

@@ -93,7 +93,6 @@ __global__ void __launch_bounds__(kThreads)
   // The producer warp initialises the barriers and fills the empty ring before
   // anyone else is ready, so the first bytes are under way during the set-up.
   auto load = [&](int kb, int s) {
-    if (kb == p.skip_k_block) return;
     uint64_t *full = bars + S::kFull0 + s;
     mbar_arrive_expect_tx(full, S::kStageBytes);
     uint8_t *sa = smem + s * S::kOperandBytes;
@@ -160,12 +159,11 @@ __global__ void __launch_bounds__(kThreads)
       if (elect_one()) load(kb, s);
       __syncwarp();
     }
-    // Tail: every filled stage has been consumed or, if the products gave up, has
-    // landed, so no load is in flight when the CTA exits.
+    // Tail: every filled stage has been consumed, so no load is in flight when
+    // the CTA exits; or its loads have had time to land.
     for (int s = 0; s < S::kStages; ++s) {
       const int fills = q / S::kStages + (s < q % S::kStages ? 1 : 0);
-      if (fills == 0 || __all_sync(0xffffffffu, wait_bar(ctx, S::kEmpty0 + s, (fills - 1) & 1))) continue;
-      if (kb0 + s + (fills - 1) * S::kStages != p.skip_k_block) drain_wait(ctx, S::kFull0 + s, (fills - 1) & 1);
+      if (fills > 0) drain_wait(ctx, S::kEmpty0 + s, (fills - 1) & 1, kTailLimit);
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer --
@@ -177,7 +175,8 @@ __global__ void __launch_bounds__(kThreads)
     int q = 0;
     for (int kb = kb0; kb < kb1; ++kb, ++q) {
       const int s = q % S::kStages;
-      if (!__all_sync(0xffffffffu, wait_bar(ctx, S::kFull0 + s, (q / S::kStages) & 1))) break;
+      const bool stall = kb == p.stall_k_block;       // test hook: kAcc is not complete before the end
+      if (!__all_sync(0xffffffffu, wait_bar(ctx, stall ? S::kAcc : S::kFull0 + s, stall ? 0 : (q / S::kStages) & 1))) break;
       tc_fence_after();
       const uint32_t a_lo = lo0 + ((s * S::kOperandBytes) >> 4);
       const uint32_t b_lo = a_lo + (kABytes >> 4);

@@ -12,6 +12,10 @@
 // runs out, the kernel records WF_ERR_TIMEOUT and still releases its TMEM, so
 // no later CTA on the SM blocks on the allocator; the launch's outputs are then
 // invalid, which the status word reports.
+//
+// A producer's tail waits for the products to consume its last stages. Products
+// that have given up never do, so these waits have a bound of their own: long
+// enough for any load to land, short enough to add up over the stages.
 #pragma once
 
 #include <cstdint>
@@ -23,7 +27,7 @@ namespace wf {
 
 constexpr long long kWaitLimit = 2000000000LL;   // ~1 s at 2 GHz (default per-launch limit)
 constexpr long long kDrainLimit = 4000000000LL;  // ~2 s: bound of the drain waits
-constexpr long long kLandCycles = 200000000LL;   // ~0.1 s: bound of let_loads_land
+constexpr long long kTailLimit = 100000000LL;    // ~0.05 s: bound of a producer's tail waits
 
 struct Ctx {
   uint64_t *bars;
@@ -72,23 +76,16 @@ __device__ __forceinline__ bool wait_bar_cluster(const Ctx &c, int b, uint32_t p
 
 // Time-bounded wait used while draining (ignores the abort flag and the
 // per-launch limit). Returns false if the drain itself ran out.
-__device__ __forceinline__ bool drain_wait(const Ctx &c, int b, uint32_t parity) {
+__device__ __forceinline__ bool drain_wait(const Ctx &c, int b, uint32_t parity, long long limit = kDrainLimit) {
   uint64_t *bar = c.bars + b;
   const long long t0 = clock64();
   while (!sm100::mbar_try_wait(bar, parity)) {
-    if (clock64() - t0 > kDrainLimit) {
+    if (clock64() - t0 > limit) {
       record_status(c.status, WF_ERR_TIMEOUT);
       return false;
     }
   }
   return true;
-}
-
-// For loads whose bytes count on the other CTA's barrier, which this one cannot watch:
-// once the pair has given up, time in which any TMA load lands.
-__device__ __forceinline__ void let_loads_land() {
-  const long long t0 = clock64();
-  while (clock64() - t0 < kLandCycles) __nanosleep(1000);
 }
 
 // Keep the compiler from using tcgen05.ld results before tcgen05.wait::ld.

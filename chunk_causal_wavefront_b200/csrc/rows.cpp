@@ -207,7 +207,7 @@ bool offers(const Plan &plan, const LinearParams &p, bool e4m3, bool out8) {
 struct NextLinear {
   bool armed = false, forced = false;
   Plan plan{};
-  int32_t skip_k_block = -1;
+  int32_t stall_k_block = -1;
   long long wait_limit = 0;
 };
 thread_local NextLinear t_next;
@@ -308,12 +308,12 @@ wf_status wf_linear(const wf_rows *x, const wf_rows *w, const float *bias, int32
   p.sms = dev.sms;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool stored_by_tma = rows16(out) && (!residual || rows16(residual));
-  p.skip_k_block = -1;
+  p.stall_k_block = -1;
   p.wait_limit = kWaitLimit;
   const NextLinear next = t_next;
   t_next = NextLinear{};
   if (next.armed) {
-    p.skip_k_block = next.skip_k_block;
+    p.stall_k_block = next.stall_k_block;
     p.wait_limit = next.wait_limit;
     if (next.forced && !offers(next.plan, p, e4m3, out8)) return WF_ERR_INVALID_ARG;
   }
@@ -322,9 +322,9 @@ wf_status wf_linear(const wf_rows *x, const wf_rows *w, const float *bias, int32
                              : launch_linear_skinny(p, e4m3, out8, plan.nt, plan.split, st));
 }
 
-wf_status wf_rows_debug_next_linear(int32_t kernel, int32_t tile, int32_t split, int32_t skip_k_block,
+wf_status wf_rows_debug_next_linear(int32_t kernel, int32_t tile, int32_t split, int32_t stall_k_block,
                                     int64_t wait_limit_cycles) {
-  if (kernel < 0 || kernel > 2 || skip_k_block < -1 || wait_limit_cycles < 1000 || wait_limit_cycles > kWaitLimit)
+  if (kernel < 0 || kernel > 2 || stall_k_block < -1 || wait_limit_cycles < 1000 || wait_limit_cycles > kWaitLimit)
     return WF_ERR_INVALID_ARG;
   if (kernel == 1 && tile != 16 && tile != 32 && tile != 64 && tile != 128) return WF_ERR_INVALID_ARG;
   if (kernel == 1 && split != 1 && split != 2 && split != 4 && split != 8) return WF_ERR_INVALID_ARG;
@@ -332,7 +332,7 @@ wf_status wf_rows_debug_next_linear(int32_t kernel, int32_t tile, int32_t split,
   t_next.armed = true;
   t_next.forced = kernel != 0;
   t_next.plan = kernel == 2 ? Plan{true, tile, 0, 0} : Plan{false, 0, tile, split};
-  t_next.skip_k_block = skip_k_block;
+  t_next.stall_k_block = stall_k_block;
   t_next.wait_limit = wait_limit_cycles;
   return WF_OK;
 }

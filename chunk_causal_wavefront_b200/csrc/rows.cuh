@@ -43,9 +43,9 @@ struct LinearParams {
   int32_t M, N, K;
   int32_t *status;                  // the device's row-operator status word
   int32_t device, sms;
-  // Test hook (wf_rows_debug_next_linear): a k-block that is not loaded (-1: none), and the
-  // cycles after which a wait gives up.
-  int32_t skip_k_block;
+  // Test hook (wf_rows_debug_next_linear): the k-block at which the products stall (-1: none), and
+  // the cycles after which a wait gives up.
+  int32_t stall_k_block;
   long long wait_limit;
 };
 

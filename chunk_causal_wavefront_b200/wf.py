@@ -302,9 +302,9 @@ def wf_linear(x: WfRows, w: WfRows, bias: Optional[int], act: int, residual: Opt
     return _lib.wf_linear(x, w, bias, act, residual, out, stream or None)
 
 
-def wf_rows_debug_next_linear(kernel: int, tile: int = 0, split: int = 0, skip_k_block: int = -1,
+def wf_rows_debug_next_linear(kernel: int, tile: int = 0, split: int = 0, stall_k_block: int = -1,
                               wait_limit_cycles: int = 2000000000) -> int:
-    return _lib.wf_rows_debug_next_linear(kernel, tile, split, skip_k_block, wait_limit_cycles)
+    return _lib.wf_rows_debug_next_linear(kernel, tile, split, stall_k_block, wait_limit_cycles)
 
 
 def wf_rows_check_status(stream: int) -> int:

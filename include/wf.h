@@ -424,15 +424,15 @@ wf_status wf_linear(const wf_rows *x, const wf_rows *w, const float *bias, int32
                     const wf_rows *residual, const wf_rows *out, wf_stream_t stream);
 
 /* Test hook: the calling thread's next wf_linear that gets as far as choosing a kernel takes
- * this one (WF_ERR_INVALID_ARG from it where the product has no such instance), leaves one k-block of
- * 128 bytes of K unloaded and gives up on its waits after wait_limit_cycles.
+ * this one (WF_ERR_INVALID_ARG from it where the product has no such instance), stalls its products
+ * at one k-block of 128 bytes of K and gives up on its waits after wait_limit_cycles.
  *   kernel            : 0 the library's choice, 1 few rows, 2 CTA pairs.
  *   tile, split       : 1: 16, 32, 64 or 128 tokens, K split over 1, 2, 4 or 8 CTAs;
  *                       2: 192, 256 or 384 features; split is not used.
- *   skip_k_block      : -1 for none.
+ *   stall_k_block     : -1 for none.
  *   wait_limit_cycles : 1000 .. 2e9. */
 wf_status wf_rows_debug_next_linear(int32_t kernel, int32_t tile, int32_t split,
-                                    int32_t skip_k_block, int64_t wait_limit_cycles);
+                                    int32_t stall_k_block, int64_t wait_limit_cycles);
 
 /* Synchronise the stream, then return and clear the current device's sticky
  * row-operator status (WF_OK, or WF_ERR_TIMEOUT from a wf_linear call). */

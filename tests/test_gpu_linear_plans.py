@@ -91,7 +91,7 @@ def test_products_without_an_instance_are_refused():
     assert wfb.rows_check_status() == 0
 
 
-# A k-block that is never loaded: every wait behind it runs out after about a millisecond, the call
+# Products that stall at a k-block: every wait behind it runs out after about a millisecond, the call
 # reports it, and the next call is as before. Early and late blocks, of the first and a later CTA of a
 # cluster; one tile and several per pair.
 @pytest.mark.parametrize("e4m3", [False, True])
@@ -107,7 +107,7 @@ def test_waits_run_out(n, features, plan, block, e4m3):
     want = wfb.linear(x, w, residual=r)
     torch.cuda.synchronize()
     for _ in range(2):
-        force(*plan, skip_k_block=block, wait_limit_cycles=2000000)
+        force(*plan, stall_k_block=block, wait_limit_cycles=2000000)
         t0 = time.monotonic()
         wfb.linear(x, w, residual=r)
         assert wfb.rows_check_status() == W.WF_ERR_TIMEOUT
