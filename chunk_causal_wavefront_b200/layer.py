@@ -21,7 +21,7 @@ import torch
 
 from . import wf as _wf
 from .pool import KVPool
-from .rows import E4M3Rows, add_rms_norm, linear, quantize_rows, refuse_gradients
+from .rows import E4M3Rows, add_rms_norm, linear, quantize_rows, refuse_gradients, rows_check_status
 
 Weight = Union[torch.Tensor, E4M3Rows]
 
@@ -51,7 +51,9 @@ class LayerWeights:
 class LayerRound:
     """Runs layers on the rounds of one pool; holds the scratch that a layer needs.
 
-    One object serves all layers of a pool, one call at a time in stream order."""
+    One object serves all layers of a pool, one call at a time in stream order. The
+    calls do not synchronise, so what goes wrong on the device (a missing publication,
+    a bounded wait that runs out) is asked for with check_status()."""
 
     def __init__(self, pool: KVPool, ffn: int, eps: float = 1e-6):
         c = pool.cfg
@@ -144,6 +146,13 @@ class LayerRound:
         self._publish(layer, h, w, None)
         self._attend(layer, h, w, None)
         return h
+
+    def check_status(self, stream=None) -> int:
+        """Synchronise, then return and clear the first error of the calls before: the pool's status,
+        or the row operators' of its device."""
+        status = self.pool.check_status(stream)
+        rows = rows_check_status(self.q_rot.device, stream)
+        return status if status != _wf.WF_OK else rows
 
     def publish_slot(self, layer: int, slot: int, h: torch.Tensor, w: LayerWeights) -> None:
         """Up to the publication of one slot's K/V (its rank delivers them next)."""

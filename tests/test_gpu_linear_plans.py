@@ -117,3 +117,20 @@ def test_waits_run_out(n, features, plan, block, e4m3):
         assert torch.equal(wfb.linear(x, w, residual=r), want)
         assert torch.equal(wfb.linear(x, w), wfb.linear(x, w))
     assert wfb.rows_check_status() == 0
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_layer_reports_both_status_words(kv):
+    from test_gpu_layer import config, make_pool, stream, weights
+    cfg = config()
+    layer, w = wfb.LayerRound(make_pool(cfg, kv), 512), weights(256, 512, 1, kv == "fp8")
+    layer.run(0, stream(cfg, 0), w)
+    assert layer.check_status() == 0
+    assert W.wf_rows_debug_next_linear(0, stall_k_block=0, wait_limit_cycles=2000000) == W.WF_OK
+    layer.run(0, stream(cfg, 0), w)
+    assert layer.check_status() == W.WF_ERR_TIMEOUT
+    assert layer.check_status() == 0
+    layer.pool.advance()
+    layer.attend_slot(0, 0, stream(cfg, 1), w)               # nothing of this round is published
+    assert layer.check_status() == W.WF_ERR_NOT_READY
+    assert layer.check_status() == 0
