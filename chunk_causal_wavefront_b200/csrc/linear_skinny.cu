@@ -62,7 +62,7 @@ struct Shape {
 };
 
 struct SkinnyGrid {
-  int f_tiles, t_tiles, n_kb, k_steps, out_block_tiles;
+  int t_tiles, n_kb, k_steps, out_block_tiles;
 };
 
 template <bool MX, int NT, int SPLIT, bool OUT8>
@@ -331,7 +331,6 @@ cudaError_t run_skinny(const LinearParams &p, cudaStream_t st) {
   SkinnyGrid g{};
   const int64_t ft = (static_cast<int64_t>(p.N) + 127) / 128, tt = (static_cast<int64_t>(p.M) + NT - 1) / NT;
   if (ft * tt * SPLIT > 0x7fffffff) return cudaErrorInvalidValue;
-  g.f_tiles = static_cast<int>(ft);
   g.t_tiles = static_cast<int>(tt);
   g.n_kb = (p.K + S::kKElems - 1) / S::kKElems;
   g.k_steps = (p.K + S::kKStep - 1) / S::kKStep;
