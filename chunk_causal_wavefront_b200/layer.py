@@ -104,8 +104,7 @@ class LayerRound:
         return "e4m3" if e4m3 else None
 
     # -- the two halves around the K/V exchange -------------------------------------------
-    def _publish(self, layer: int, h: torch.Tensor, w: LayerWeights, slot: Optional[int]) -> None:
-        to = self._check(h, w)
+    def _publish(self, layer: int, h: torch.Tensor, w: LayerWeights, slot: Optional[int], to: Optional[str]) -> None:
         pool, hidden = self.pool, self.hidden
         x = self._rows(h, slot)
         if (slot is None and to is None and pool.cfg.dtype == _wf.WF_DTYPE_BF16
@@ -127,8 +126,7 @@ class LayerRound:
         else:
             pool.publish_slot(layer, slot, *self._qkv, self.q_rot)
 
-    def _attend(self, layer: int, h: torch.Tensor, w: LayerWeights, slot: Optional[int]) -> None:
-        to = self._check(h, w)
+    def _attend(self, layer: int, h: torch.Tensor, w: LayerWeights, slot: Optional[int], to: Optional[str]) -> None:
         pool = self.pool
         if slot is None:
             pool.attention(layer, self.q_rot, self.att)
@@ -143,8 +141,9 @@ class LayerRound:
     # -- calls ------------------------------------------------------------------------------
     def run(self, layer: int, h: torch.Tensor, w: LayerWeights) -> torch.Tensor:
         """The layer on every live slot of the pool's round; updates h in place."""
-        self._publish(layer, h, w, None)
-        self._attend(layer, h, w, None)
+        to = self._check(h, w)
+        self._publish(layer, h, w, None, to)
+        self._attend(layer, h, w, None, to)
         return h
 
     def check_status(self, stream=None) -> int:
@@ -156,9 +155,9 @@ class LayerRound:
 
     def publish_slot(self, layer: int, slot: int, h: torch.Tensor, w: LayerWeights) -> None:
         """Up to the publication of one slot's K/V (its rank delivers them next)."""
-        self._publish(layer, h, w, slot)
+        self._publish(layer, h, w, slot, self._check(h, w))
 
     def attend_slot(self, layer: int, slot: int, h: torch.Tensor, w: LayerWeights) -> torch.Tensor:
         """From the slot's attention on, once the deliveries into this pool have landed."""
-        self._attend(layer, h, w, slot)
+        self._attend(layer, h, w, slot, self._check(h, w))
         return h
