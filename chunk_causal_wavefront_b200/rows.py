@@ -83,6 +83,8 @@ class E4M3Rows:
 
     def first(self, rows: int) -> "E4M3Rows":
         """The first rows, sharing memory."""
+        if not 0 <= rows <= self.codes.shape[0]:
+            raise ValueError(f"there are {self.codes.shape[0]} rows, not {rows}")
         return E4M3Rows(self.codes[:rows], self.scales)
 
     def span(self, start: int, stop: int) -> "E4M3Rows":
