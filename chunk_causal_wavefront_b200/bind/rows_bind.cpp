@@ -43,7 +43,8 @@ const Tensor &plain(PyObject *o, at::ScalarType a, at::ScalarType b, bool *ok) {
   if (!t.is_cuda() || t.layout() != at::kStrided || !t.has_storage() || (type != a && type != b) || t.dim() < 1 ||
       !t.is_contiguous() || t.is_conj() || t.is_neg() || t.size(-1) == 0 ||
       t.get_device() != c10::cuda::current_device() ||
-      (c10::GradMode::is_enabled() && t.requires_grad()) || t._fw_grad(/*level=*/0).defined())
+      (c10::GradMode::is_enabled() && t.requires_grad()) ||
+      (t.unsafeGetTensorImpl()->autograd_meta() && t._fw_grad(/*level=*/0).defined()))
     *ok = false;
   return t;
 }

@@ -299,6 +299,9 @@ def add_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *,
                  out_dtype=None, stream=None) -> Union[Operand, Tuple[Operand, torch.Tensor]]:
     """s = x + residual; out = s / sqrt(mean(s^2) + eps) * weight, row by row.
 
+    Computed in fp32 (the sum of squares in 64 bits): a row with a value beyond 2^63
+    or so has an infinite mean, and out is 0 there.
+
     Without a residual returns out, with one (out, s). out has x's type, or is
     E4M3Rows with out_dtype="e4m3" (or out=E4M3Rows). sum_out may be x or
     residual: the residual stream is then updated in place. weight is float32.
@@ -351,10 +354,11 @@ def linear(x: Operand, w: Operand, bias: Optional[torch.Tensor] = None, *, act: 
            out_dtype=None, stream=None) -> Operand:
     """act(x w^T + bias) + residual on the tensor cores, accumulated in fp32.
 
-    x [..., K] and w [N, K] are both bf16 or both E4M3Rows; bias is float32 [N];
-    act is "none", "gelu" (tanh form) or "silu". The result is bf16 [..., N], or
-    E4M3Rows with out_dtype="e4m3" (or out=E4M3Rows), then without a residual.
-    out may be residual itself.
+    x [..., K] and w [N, K] are both bf16 or both E4M3Rows, their rows at multiples of
+    16 bytes (contiguous bf16: K a multiple of 8); bias is float32 [N]; act is "none",
+    "gelu" (tanh form) or "silu". The result is bf16 [..., N], or E4M3Rows with
+    out_dtype="e4m3" (or out=E4M3Rows), then without a residual. out may be residual
+    itself.
     """
     code = _ACTS.get(act)
     if code is None:

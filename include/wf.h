@@ -395,7 +395,8 @@ wf_status wf_dequantize_rows(const wf_rows *x, const wf_rows *out, wf_stream_t s
 
 /* Residual addition and root-mean-square norm of every row:
  *     s = x + residual,   sum = s,   out = s / sqrt(mean(s^2) + eps) * weight
- * in fp32, each output rounded once (out from the unrounded s).
+ * in fp32, each output rounded once (out from the unrounded s). The squares are fp32 too, a few
+ * at a time: a row with a value beyond 2^63 or so has an infinite mean, and out is 0 there.
  *   x, residual : bf16 or fp32, the same type and shape; residual may be NULL.
  *   weight      : fp32 [cols], or NULL for ones.
  *   eps         : finite, >= 0.
