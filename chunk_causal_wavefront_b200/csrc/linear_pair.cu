@@ -16,7 +16,8 @@
 // features that share the row operand (384 wide): 29 % fewer bytes per product,
 // but each half has one accumulator. The halves' products are reordered at a
 // tile's ends to give the epilogue time; what of it stays exposed, about 3 us per
-// tile, pays only for long K: 23400 x 1536 x 6144 E4M3 206 (192) and 194 us (384)
+// tile, pays only for long K (at K = 256 and below the epilogue sets the time of every
+// tile: 23400 x 1536 x 256 bf16 with residual 31 (192) and 36 us (256)): 23400 x 1536 x 6144 E4M3 206 (192) and 194 us (384)
 // under the power cap, x 1536 x 1536 bf16 100 (256), 102 (384) and 105 us (192). 512
 // wide (two halves of 256) was never the best by more than 2 %.
 // Tiles are walked in groups of 8 row tiles, feature tiles slowest inside a
@@ -44,8 +45,9 @@
 //                      thread finds its scale without leaving its registers.
 //   Output or residual rows that TMA cannot reach (an odd N, a stride that is not a
 //   multiple of 16 bytes) take DIRECT: the staging rows are written and read with
-//   a lane per column, 64 bytes of a row at a time; 23400 x 1535 x 1536 bf16 100 us, with
-//   residual 140 (1536 features through TMA: 87).
+//   a lane per column, 64 bytes of a row at a time, and the residual is loaded in the step
+//   that adds it; 23400 x 1535 x 1536 bf16 93-103 us, with residual 114-139, by tile (1536
+//   features through TMA: 83-87).
 // Every wait is bounded; a timeout is recorded in the row-operator status word.
 #include <cuda.h>
 #include <cuda_bf16.h>

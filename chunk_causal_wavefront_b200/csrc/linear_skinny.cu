@@ -19,10 +19,10 @@
 //   Two CTAs share an SM up to 64 tokens. Each holds 81 KB of shared memory or
 //   more, so no CTA of another clustered kernel (all hold over 200 KB) fits beside
 //   it: two clusters never wait for each other's tensor memory.
-//   Measured (captured graph, weights in HBM): 1 x 6144 x 1536 bf16 6.8 us (18.9 MB;
-//   the weights alone 2.9 us at 6.55 TB/s, the rest is the latency of launch, first
-//   loads, cluster barriers and last stores), 24 x 5120 x 5120 E4M3 9.5 us, 64 x 1536
-//   x 1536 bf16 5.9 us, 1111 x 1000 x 1544 13.7 us (against 14.6 on CTA pairs).
+//   Measured (captured graph or burst, weights in HBM): 1 x 6144 x 1536 bf16 6.5-7.0 us
+//   (18.9 MB; the weights alone 2.9 us at 6.55 TB/s, the rest is the latency of launch,
+//   first loads, cluster barriers and last stores), 24 x 5120 x 5120 E4M3 9.0-9.4 us, 64 x
+//   1536 x 1536 bf16 5.3-5.9 us, 1111 x 1000 x 1544 13.3-14.2 us (against 14.6-16 on CTA pairs).
 // Every wait is bounded; a timeout is recorded in the row-operator status word.
 #include <cuda.h>
 #include <cuda_bf16.h>

@@ -135,7 +135,11 @@ wf_status convert(const wf_rows *x, const wf_rows *out, bool to_e4m3, cudaStream
 
 // Which kernel a product takes, and its tile: the smallest estimate of the time in
 // microseconds, from figures measured on a B200 (large products under its power
-// cap, small ones at 1965 MHz with weights in HBM).
+// cap, small ones at 1965 MHz with weights in HBM). Where an epilogue is longer than its
+// tile's products (K of a few hundred, or rows that TMA cannot reach) the estimate does
+// not know it, and 192 features can be faster than the tile taken: 23400 x 1535 x 1536 bf16
+// with residual 114 us against 135 (384). Waves of wide clusters cost more than it says:
+// 512 x 1536 x 6144 takes 39 us with K split over eight CTAs, 23 over two.
 struct Plan {
   bool pair;
   int bn, nt, split;

@@ -3,9 +3,11 @@
 //
 // All three read each element once and write each result once; HBM bounds them.
 // Measured, of the 6554 GB/s that a copy reaches: norm with residual, 23400 x 1536
-// bf16 48.0 us (91 %), 23400 x 5120 to E4M3 143 us (90 %); without residual 27.7 us
-// (79 %: half the bytes in flight per row); 23400 x 5120 bf16 to E4M3 58 us (95 %)
-// and back 60 us (92 %); a single row 2.7 us, all of it launch and latency.
+// bf16 48-50 us (88-91 %), fp32 104 us (85 %), 23400 x 5120 bf16 to E4M3 144-146 us
+// (88-90 %); without residual 23400 x 1536 bf16 27-28 us (78-81 %: half the bytes in
+// flight per row), fp32 51 us (86 %), 23400 x 5120 fp32 212 us (69 %); 23400 x 5120 bf16
+// to E4M3 58 us (95 %) and back 60-63 us (88-92 %); a single row 2.7 us, all of it launch
+// and latency.
 //
 // Norm: s = x + residual, out = s / sqrt(mean(s^2) + eps) * weight.
 //   A row stays in registers between its one read and its one write: up to 8
@@ -241,8 +243,8 @@ __global__ void __launch_bounds__(kNormThreads, (sizeof(T) == 2 ? 2 : 1) + (CH <
 // (the strange elements are dropped) unless it leaves the operand, and stored
 // element by element. The weight is staged in shared memory: at eight loads of it per
 // chunk that no vector load can replace, and a select for each, this bounds the kernel:
-// 23400 x 1001 bf16 37 us, with residual 48 (60 % of HBM; element by element 53 and
-// 70), 23400 x 5119 159 and 190 us (193 and 352).
+// 23400 x 1001 bf16 37-38 us, with residual 47-49 (58-60 % of HBM; element by element 53
+// and 70), 23400 x 5119 160-163 and 191-194 us (193 and 352).
 template <typename T, int CH>
 __global__ void __launch_bounds__(kNormThreads, (sizeof(T) == 2 ? 2 : 1) + (CH < 4)) norm_shift_kernel(const NormParams p, const int wpr) {
   __shared__ double part[2][kNormThreads / 32];
@@ -364,7 +366,8 @@ __global__ void __launch_bounds__(kNormThreads, (sizeof(T) == 2 ? 2 : 1) + (CH <
 // longer rows are read twice, a thread's squares summed in fp32 sixteen at a time and
 // in 64 bits from there (a row may have 2^24 columns per thread, and an fp32 sum
 // stands still at that many). A thread's elements are the same in both readings, so
-// outputs may be the inputs.
+// outputs may be the inputs. A block and a barrier per row: 23400 x 33 bf16 36 us; 23400 x
+// 8200 bf16 with residual 555 us (42 % of HBM).
 constexpr int kAnyThreads = 128;
 constexpr int kAnyKeep = 16;
 
