@@ -79,6 +79,21 @@ def test_norm_to_e4m3_without_eps_near_zero():
     np.testing.assert_array_equal(got, np.broadcast_to(f64(w), (3, 64)))
 
 
+def test_norm_to_e4m3_of_an_infinite_factor():
+    """Without eps, squares below fp32's range give a mean of zero and an infinite factor; to E4M3 as to
+    fp32 the values are infinities of s * weight's sign, and NaN where that is zero."""
+    x = torch.full((2, 96), 2.0 ** -80, device="cuda")
+    x[1] = -x[1]
+    w = torch.linspace(0.5, 3.0, 96, device="cuda")
+    w[::2] = -w[::2]
+    w[5], x[0, 70] = 0.0, 0.0
+    want = f64(wfb.add_rms_norm(x, w, eps=0.0))
+    assert np.isinf(np.delete(want, [5, 70], axis=1)).all() and np.isnan(want[0, [5, 70]]).all()
+    np.testing.assert_array_equal(f64(wfb.add_rms_norm(x, w, eps=0.0, out_dtype="e4m3").dequantize(dtype=F32)), want)
+    x = torch.full((2, 8224), 2.0 ** -80, device="cuda")                     # the kernel for any row
+    assert (wfb.add_rms_norm(x, eps=0.0, out_dtype="e4m3").dequantize(dtype=F32) == float("inf")).all()
+
+
 def factor_of(x, eps=0.0):
     """The rows' factor: computed in 64 bits from the exact sum, rounded once. (The kernel's 64-bit
     reciprocal root may be an ulp of 64 bits away, which changes the fp32 rounding of one row in 2^27.)"""
