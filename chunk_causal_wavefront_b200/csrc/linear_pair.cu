@@ -198,7 +198,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<MX, BN, HALVES
     // load of this CTA is in flight when it exits; or they have had time to land.
     for (int s = 0; s < S::kStages && q > 0; ++s) {
       const int fills = q / S::kStages + (s < q % S::kStages ? 1 : 0);
-      if (fills > 0) drain_wait(ctx, S::kEmpty0 + s, (fills - 1) & 1, kTailLimit);
+      if (fills > 0) tail_wait(ctx, S::kEmpty0 + s, (fills - 1) & 1);
     }
   } else if (warp == S::kMmaWarp) {
     // ---------------------------------------------------------- MMA issuer --

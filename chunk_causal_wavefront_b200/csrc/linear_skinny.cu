@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kThreads)
     // the CTA exits; or its loads have had time to land.
     for (int s = 0; s < S::kStages; ++s) {
       const int fills = q / S::kStages + (s < q % S::kStages ? 1 : 0);
-      if (fills > 0) drain_wait(ctx, S::kEmpty0 + s, (fills - 1) & 1, kTailLimit);
+      if (fills > 0) tail_wait(ctx, S::kEmpty0 + s, (fills - 1) & 1);
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer --

@@ -76,16 +76,25 @@ __device__ __forceinline__ bool wait_bar_cluster(const Ctx &c, int b, uint32_t p
 
 // Time-bounded wait used while draining (ignores the abort flag and the
 // per-launch limit). Returns false if the drain itself ran out.
-__device__ __forceinline__ bool drain_wait(const Ctx &c, int b, uint32_t parity, long long limit = kDrainLimit) {
+__device__ __forceinline__ bool drain_wait(const Ctx &c, int b, uint32_t parity) {
   uint64_t *bar = c.bars + b;
   const long long t0 = clock64();
   while (!sm100::mbar_try_wait(bar, parity)) {
-    if (clock64() - t0 > limit) {
+    if (clock64() - t0 > kDrainLimit) {
       record_status(c.status, WF_ERR_TIMEOUT);
       return false;
     }
   }
   return true;
+}
+
+// Wait of a producer's tail. It records nothing: products that have given up have said
+// so, and those that have not are waited for by their own completion.
+__device__ __forceinline__ void tail_wait(const Ctx &c, int b, uint32_t parity) {
+  uint64_t *bar = c.bars + b;
+  const long long t0 = clock64();
+  while (!sm100::mbar_try_wait(bar, parity))
+    if (clock64() - t0 > kTailLimit) return;
 }
 
 // Keep the compiler from using tcgen05.ld results before tcgen05.wait::ld.
