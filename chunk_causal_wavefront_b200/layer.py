@@ -89,7 +89,13 @@ class LayerRound:
             m = getattr(w, name)
             if tuple(m.shape) != shape or not (e4m3 or m.dtype == torch.bfloat16):
                 raise ValueError(f"{name} must be {list(shape)} in bf16 or E4M3 rows, not {list(m.shape)}")
+            c = m.codes if e4m3 else m
+            if (c.stride(1) != 1 or c.stride(0) < shape[1] or c.stride(0) * c.element_size() % 16
+                    or c.data_ptr() % 16 or (e4m3 and m.scales.data_ptr() % 16)):
+                raise ValueError(f"{name} must have contiguous rows that start at multiples of 16 bytes")
             given.append((name, m))
+        if ffn % 8:
+            raise ValueError(f"the feed-forward's {ffn} features are not a multiple of 8")
         for name, n in (("norm1", hidden), ("norm2", hidden), ("b_out", hidden), ("b_up", ffn), ("b_down", hidden)):
             v = getattr(w, name)
             if v is None:

@@ -69,6 +69,23 @@ def test_e4m3_weights(layer):
     refuses(layer, "all bf16 or all", **{**w, "w_up": weights().w_up})
 
 
+# What the products would refuse, one of them after h has been changed.
+@pytest.mark.parametrize("name,shape", [("w_out", (HIDDEN, HIDDEN)), ("w_up", (FFN, HIDDEN)), ("w_down", (HIDDEN, FFN))])
+def test_rows_of_weights(layer, name, shape):
+    n, k = shape
+    bf16 = dict(dtype=torch.bfloat16)
+    for bad in (torch.zeros(n * k + 1, **bf16)[1:].view(n, k), torch.zeros(n, k + 1, **bf16)[:, :k],
+                torch.zeros(k, n, **bf16).t(), torch.zeros(1, k, **bf16).expand(n, k)):
+        refuses(layer, name, **{name: bad})
+    passes(layer, **{name: torch.zeros(n, k + 8, **bf16)[:, :k]})             # strided rows are fine
+
+
+def test_odd_feed_forward(layer):
+    wide = torch.zeros(HIDDEN, FFN, dtype=torch.bfloat16)[:, :FFN - 3]
+    refuses(layer, "multiple of 8", w_up=torch.zeros(FFN - 3, HIDDEN, dtype=torch.bfloat16), w_down=wide,
+            b_up=torch.zeros(FFN - 3))
+
+
 @pytest.mark.parametrize("name,n", [("norm1", HIDDEN), ("norm2", HIDDEN), ("b_out", HIDDEN), ("b_up", FFN),
                                     ("b_down", HIDDEN)])
 def test_vectors(layer, name, n):
