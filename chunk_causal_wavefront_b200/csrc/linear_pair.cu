@@ -16,10 +16,11 @@
 // features that share the row operand (384 wide): 29 % fewer bytes per product,
 // but each half has one accumulator. The halves' products are reordered at a
 // tile's ends to give the epilogue time; what of it stays exposed, about 3 us per
-// tile, pays only for long K (at K = 256 and below the epilogue sets the time of every
-// tile: 23400 x 1536 x 256 bf16 with residual 31 (192) and 36 us (256)): 23400 x 1536 x 6144 E4M3 206 (192) and 194 us (384)
+// tile, pays only for long K: 23400 x 1536 x 6144 E4M3 206 (192) and 194 us (384)
 // under the power cap, x 1536 x 1536 bf16 100 (256), 102 (384) and 105 us (192). 512
-// wide (two halves of 256) was never the best by more than 2 %.
+// wide (two halves of 256) was never the best by more than 2 %. At K = 256 and below
+// the epilogue sets the time of every tile: 23400 x 1536 x 256 bf16 with residual 31
+// (192) and 36 us (256).
 // Tiles are walked in groups of 8 row tiles, feature tiles slowest inside a
 // group, so that the tiles in flight cover a near-square patch of the output and
 // both operands are re-read from L2.
